@@ -15,6 +15,13 @@
  *   moe_expand_rows_mxfp8 expand with MXFP8 quantisation (E8M0 scale per 32 columns)
  *   moe_route_expand_fp8 moe_route_padded + moe_expand_rows_fp8 in one call
  *   moe_route_expand_mxfp8 moe_route_padded + moe_expand_rows_mxfp8 in one call
+ *   moe_rmsnorm      root-mean-square norm with the residual's addition; also
+ *                    with FP8 (moe_rmsnorm_fp8) or MXFP8 (moe_rmsnorm_mxfp8)
+ *                    output
+ *   moe_decode_layer the whole layer for a few tokens in two launches, experts'
+ *                    products included, on bf16 weights;
+ *                    moe_decode_layer_mxfp4 on 4-bit weights
+ *   moe_linear_mxfp4 product of a few tokens with 4-bit weights
  *
  * The problem statement these calls follow:
  *   - "CuTeDSL at Perplexity" (Perplexity blog), section "Mixture of Experts
@@ -308,6 +315,112 @@ moe_status moe_swiglu(const uint16_t* h, int32_t R, int32_t I, uint16_t* act, vo
  * MOE_ERR_UNSUPPORTED (T*H/8 >= 2^31), MOE_ERR_HIP. */
 moe_status moe_combine(const uint16_t* y, const float* topk_weights, const int32_t* dest_of_src,
                        int32_t T, int32_t H, int32_t k, uint16_t* out, void* stream);
+
+/* ------------------------------------------------------------------- norm */
+
+#define MOE_NORM_H_MAX 65536 /* widest normalised row                               */
+
+/* Root-mean-square norm of the residual stream, before the router and the
+ * experts.  For each row t, in fp32:
+ *   s = x[t, :] + residual[t, :]          (residual may be NULL: s = x[t, :])
+ *   n = s / sqrt(mean(s^2) + eps) * weight
+ *   residual_out[t, :] = bf16(s)          (NULL: not written)
+ *   out[t, :] = bf16(n)
+ * Each result is rounded once, to nearest even: n is formed from the unrounded
+ * s.  The row sum is formed in fp32, in an order that depends on H alone; rows
+ * whose squares pass fp32's range are scaled first.  A row with an infinity or
+ * a NaN normalises as the formula does (NaN at the infinities and 0 beside
+ * them; a NaN makes the whole row NaN).
+ * x, residual, residual_out, out bf16 [T, H]; weight bf16 [H].  H % 8 == 0,
+ * H <= MOE_NORM_H_MAX; every pointer 16-byte aligned.  eps must be finite and
+ * a positive normal fp32.  residual_out may be the very buffer residual (the
+ * residual stream updated in place); without a residual it must be NULL.  T = 0
+ * is a no-op.  Errors: MOE_ERR_NULL, MOE_ERR_SHAPE, MOE_ERR_ALIGN,
+ * MOE_ERR_UNSUPPORTED (H, eps, T*H/8 >= 2^31), MOE_ERR_HIP. */
+moe_status moe_rmsnorm(const uint16_t* x, const uint16_t* residual, const uint16_t* weight, int32_t T, int32_t H,
+                       float eps, uint16_t* residual_out, uint16_t* out, void* stream);
+
+/* moe_rmsnorm with FP8 output: n (fp32, not rounded to bf16 first) quantised
+ * per `group` consecutive columns in the format of moe_expand_rows_fp8:
+ *   amax = max |n[c]| over the group; scale = fp32(amax / 448)
+ *   code = E4M3(clamp(fp32(n[c] * fp32(448 / amax)), -448, 448)), nearest-even
+ * (0 for an all-zero group).  A group with a NaN or an infinity in n has a NaN
+ * scale and NaN codes (0x7F).  out, bf16(n), is written too unless NULL: the
+ * row for the router beside the codes for the experts.
+ * codes uint8 [T, H]; scales fp32 [T, H/group]; group a power of two in
+ * [8, 512] dividing H.  Alignment: bf16 tensors 16 bytes, codes 8, scales 4.
+ * Errors: moe_rmsnorm's, and those of moe_expand_rows_fp8 for group. */
+moe_status moe_rmsnorm_fp8(const uint16_t* x, const uint16_t* residual, const uint16_t* weight, int32_t T, int32_t H,
+                           float eps, int32_t group, uint16_t* residual_out, uint16_t* out, uint8_t* codes,
+                           float* scales, void* stream);
+
+/* moe_rmsnorm with MXFP8 output: n (fp32) quantised per 32 consecutive columns
+ * in the format of moe_expand_rows_mxfp8 (E8M0 scale byte e + 127,
+ * e = max(floor(log2 amax) - 8, -127), codes E4M3(clamp(n / 2^e, +-448))).  A
+ * block with a NaN or an infinity in n has the scale byte 255 (NaN) and codes
+ * 0x7F.  codes uint8 [T, H]; scales uint8 [T, H/32]; H % 32 == 0; otherwise as
+ * moe_rmsnorm_fp8. */
+moe_status moe_rmsnorm_mxfp8(const uint16_t* x, const uint16_t* residual, const uint16_t* weight, int32_t T, int32_t H,
+                             float eps, uint16_t* residual_out, uint16_t* out, uint8_t* codes, uint8_t* scales,
+                             void* stream);
+
+/* ------------------------------------------------------- few-token products */
+
+#define MOE_DECODE_T_MAX 64        /* tokens of the few-token products              */
+#define MOE_DECODE_WIDTH_MAX (1 << 20) /* H, I, K and N of the few-token products    */
+
+/* The whole Mixture-of-Experts layer for T <= MOE_DECODE_T_MAX tokens, in two
+ * launches: routing as moe_route, then for every token t and slot j with
+ * e = topk_ids[t, j]
+ *   (g | u) = w_gate_up[e] x[t]      (fp32; g rows 0..I-1, u rows I..2I-1)
+ *   act     = bf16(silu(g) * u)
+ *   y_j     = w_down[e] act          (fp32)
+ *   out[t]  = bf16(sum_j topk_weights[t, j] * y_j)   (fp32, in j order)
+ * act is rounded because the second product takes bf16 operands; nothing else
+ * is, before out.  Reads the weights of the experts that the batch picks, once
+ * each.  The same call gives the same bits every time.
+ * Layouts: logits fp32 [T, E], bias fp32 [E] or NULL, x bf16 [T, H], w_gate_up
+ * bf16 [E, 2I, H], w_down bf16 [E, H, I], topk_ids int32 [T, k], topk_weights
+ * fp32 [T, k], out bf16 [T, H].  H % 8 == 0 and I % 8 == 0; x, the weights, out
+ * and the workspace 16-byte aligned; logits, bias, ids and topk_weights 4-byte.
+ * Limits: those of moe_route on E and k; H, I <= MOE_DECODE_WIDTH_MAX.
+ * The workspace must hold moe_decode_layer_workspace_bytes(T, E, k, I) bytes
+ * (0 for invalid arguments); it needs no initialisation, and calls that can
+ * overlap on the device (on two streams, or in graphs that run at once) need
+ * one each.  T = 0 is a no-op.  Logits and bias must be finite, as for
+ * moe_route.  Errors: MOE_ERR_NULL, MOE_ERR_SHAPE, MOE_ERR_ALIGN,
+ * MOE_ERR_UNSUPPORTED (T, E, k, H, I), MOE_ERR_WORKSPACE, MOE_ERR_HIP. */
+size_t moe_decode_layer_workspace_bytes(int32_t T, int32_t E, int32_t k, int32_t I);
+moe_status moe_decode_layer(const float* logits, const float* bias, int32_t T, int32_t E, int32_t k,
+                            const uint16_t* x, int32_t H, const uint16_t* w_gate_up, const uint16_t* w_down,
+                            int32_t I, int32_t* topk_ids, float* topk_weights, uint16_t* out, void* workspace,
+                            size_t workspace_bytes, void* stream);
+
+/* moe_decode_layer on MXFP4 weights (OCP microscaling): E2M1 codes, two to a
+ * byte with the lower column in the low four bits, and one E8M0 scale byte per
+ * 32 consecutive columns of a row:
+ *   w[r, c] = e2m1(code[r, c]) * 2^(scales[r, c / 32] - 127)
+ * (scale byte 255: NaN).  Every such value up to scale byte 252 is a bf16, and
+ * the products are those of bf16 weights with these values; beyond it, values
+ * that pass bf16's range are infinite.
+ * w_gate_up uint8 [E, 2I, H/2], s_gate_up uint8 [E, 2I, H/32], w_down uint8
+ * [E, H, I/2], s_down uint8 [E, H, I/32]; H % 32 == 0 and I % 32 == 0; the codes
+ * 16-byte aligned.  Otherwise as moe_decode_layer. */
+moe_status moe_decode_layer_mxfp4(const float* logits, const float* bias, int32_t T, int32_t E, int32_t k,
+                                  const uint16_t* x, int32_t H, const uint8_t* w_gate_up, const uint8_t* s_gate_up,
+                                  const uint8_t* w_down, const uint8_t* s_down, int32_t I, int32_t* topk_ids,
+                                  float* topk_weights, uint16_t* out, void* workspace, size_t workspace_bytes,
+                                  void* stream);
+
+/* Product of T <= MOE_DECODE_T_MAX tokens with MXFP4 weights (a shared
+ * expert's or another dense projection's, in the format above):
+ *   y[t, n] = bf16(sum_k x[t, k] * w[n, k])      (fp32 sum)
+ * x bf16 [T, K]; w uint8 [N, K/2]; scales uint8 [N, K/32]; y bf16 [T, N].
+ * K % 32 == 0; any N >= 1; x and w 16-byte aligned, y 2-byte.  K and N at most
+ * MOE_DECODE_WIDTH_MAX.  T = 0 is a no-op.  Errors: MOE_ERR_NULL,
+ * MOE_ERR_SHAPE, MOE_ERR_ALIGN, MOE_ERR_UNSUPPORTED (T, K, N), MOE_ERR_HIP. */
+moe_status moe_linear_mxfp4(const uint16_t* x, int32_t T, int32_t K, const uint8_t* w, const uint8_t* scales,
+                            int32_t N, uint16_t* y, void* stream);
 
 /* -------------------------------------------------------------- utilities */
 

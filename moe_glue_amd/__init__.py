@@ -15,6 +15,11 @@ Four calls, each a thin wrapper over the C ABI of the HIP library
     expand_rows_fp8(x, dest, k, group) expand with FP8 E4M3 quantisation per column group
     expand_rows_mxfp8(x, dest, k)    expand with MXFP8 quantisation (E8M0 scale per 32 columns)
     route_expand_fp8 / route_expand_mxfp8  route + the quantising expand in one call
+    rmsnorm(x, weight, residual)       root-mean-square norm with the residual's addition
+    rmsnorm_fp8 / rmsnorm_mxfp8        the same with E4M3 codes and fp32 or E8M0 scales out
+    decode_layer(logits, k, x, w_gate_up, w_down)  the whole layer for T <= 64 tokens, experts included
+    decode_layer_mxfp4(...)            the same on 4-bit (MXFP4) expert weights
+    linear_mxfp4(x, w, scales)         product of T <= 64 tokens with MXFP4 weights
 
 Tensors are torch CUDA (HIP) tensors; bf16 tensors use torch.bfloat16.  Work
 is enqueued on torch's current stream and nothing synchronises.  Every call
@@ -23,13 +28,16 @@ can run the path without allocating.
 """
 from __future__ import annotations
 
-from ._binding import (E_MAX, EXPORTED, K_MAX, LIB_PATH, MoEGlueArgumentError, MoEGlueError, check,  # noqa: F401
-                       load)
+from ._binding import (DECODE_T_MAX, E_MAX, EXPORTED, K_MAX, LIB_PATH, NORM_H_MAX,  # noqa: F401
+                       MoEGlueArgumentError, MoEGlueError, check, load)
 
 __all__ = ["route", "route_workspace_bytes", "alloc_route_outputs", "route_padded", "padded_rows", "expand_rows",
            "expand_rows_fp8", "expand_rows_mxfp8",
            "route_expand", "route_expand_noalloc", "noalloc_scratch_bytes", "route_expand_padded", "route_expand_fp8", "route_expand_mxfp8", "swiglu", "combine",
-           "copy_probe", "mix_probe", "MoEGlueError", "MoEGlueArgumentError", "E_MAX", "K_MAX"]
+           "rmsnorm", "rmsnorm_fp8", "rmsnorm_mxfp8", "decode_layer", "decode_layer_mxfp4",
+           "decode_layer_workspace_bytes", "alloc_decode_outputs", "linear_mxfp4",
+           "copy_probe", "mix_probe", "MoEGlueError", "MoEGlueArgumentError", "E_MAX", "K_MAX",
+           "NORM_H_MAX", "DECODE_T_MAX"]
 
 
 def _torch():
@@ -433,6 +441,211 @@ def combine(y, topk_weights, dest_of_src, out=None):
             raise MoEGlueArgumentError(2, f"out must be [{T}, {H}]")
     st = load().moe_combine(_ptr(y), _ptr(topk_weights), _ptr(dest_of_src), T, H, k, _ptr(out), _stream(y.device))
     check(st, "moe_combine")
+    return out
+
+
+def _same_device(named, device) -> None:
+    """Every given tensor lives on `device` (a kernel runs on one GPU)."""
+    for name, t in named:
+        if t is not None and t.device != device:
+            raise MoEGlueArgumentError(2, f"{name} is on {t.device}, expected {device}")
+
+
+def _check_shape(name: str, t, dtype, shape: tuple, device) -> None:
+    """t: a contiguous GPU tensor of this dtype and shape on `device`."""
+    if t is not None and t.dtype == dtype and t.shape == shape and t.device == device and t.is_contiguous():
+        return
+    _need_gpu(name, t, dtype, len(shape))
+    if tuple(t.shape) != tuple(shape):
+        raise MoEGlueArgumentError(2, f"{name} is {list(t.shape)}, expected {list(shape)}")
+    _same_device([(name, t)], device)
+
+
+def _enqueue(fn: str, device, *args) -> None:
+    """Call the library on `device`'s current stream, with `device` current (the
+    default stream's handle names no device of its own)."""
+    torch = _torch()
+    call = getattr(load(), fn)
+    if torch.cuda.current_device() == device.index:
+        check(call(*args, _stream(device)), fn)
+        return
+    with torch.cuda.device(device):
+        check(call(*args, _stream(device)), fn)
+
+
+def _norm_args(x, weight, residual, residual_out, out, normed_name: str):
+    """Checks shared by the norms; returns (T, H, residual_out)."""
+    torch = _torch()
+    bf16 = torch.bfloat16
+    _need_gpu("x", x, bf16, 2)
+    shape, dev = x.shape, x.device
+    _check_shape("weight", weight, bf16, (shape[1],), dev)
+    if residual is not None:
+        _check_shape("residual", residual, bf16, shape, dev)
+        if residual_out is None:
+            residual_out = torch.empty_like(x)
+        else:
+            _check_shape("residual_out", residual_out, bf16, shape, dev)
+    elif residual_out is not None:
+        raise MoEGlueArgumentError(1, "residual_out without residual")
+    if out is not None:
+        _check_shape(normed_name, out, bf16, shape, dev)
+    return shape[0], shape[1], residual_out
+
+
+def rmsnorm(x, weight, residual=None, eps: float = 1e-6, out=None, residual_out=None):
+    """Root-mean-square norm of x (+ residual); returns (out, residual_out), the
+    latter None without a residual.  residual_out may be `residual` itself.  See
+    moe_rmsnorm in include/moe_glue.h."""
+    T, H, residual_out = _norm_args(x, weight, residual, residual_out, out, "out")
+    if out is None:
+        out = _torch().empty_like(x)
+    _enqueue("moe_rmsnorm", x.device, _ptr(x), _ptr(residual), _ptr(weight), T, H, eps, _ptr(residual_out), _ptr(out))
+    return out, residual_out
+
+
+def rmsnorm_fp8(x, weight, group: int, residual=None, eps: float = 1e-6, out=None, scales=None, residual_out=None,
+                normed=None):
+    """rmsnorm() with E4M3 codes and one fp32 scale per `group` columns; returns
+    (codes uint8 [T, H], scales fp32 [T, H/group], residual_out).  `normed`: a
+    bf16 [T, H] tensor that receives rmsnorm()'s row as well.  See
+    moe_rmsnorm_fp8 in include/moe_glue.h."""
+    torch = _torch()
+    T, H, residual_out = _norm_args(x, weight, residual, residual_out, normed, "normed")
+    if group < 1 or H % group != 0:
+        raise MoEGlueArgumentError(2, f"group={group} does not divide H={H}")
+    if out is None:
+        out = torch.empty((T, H), dtype=torch.uint8, device=x.device)
+    else:
+        _check_shape("out", out, torch.uint8, (T, H), x.device)
+    if scales is None:
+        scales = torch.empty((T, H // group), dtype=torch.float32, device=x.device)
+    else:
+        _check_shape("scales", scales, torch.float32, (T, H // group), x.device)
+    _enqueue("moe_rmsnorm_fp8", x.device, _ptr(x), _ptr(residual), _ptr(weight), T, H, eps, group,
+             _ptr(residual_out), _ptr(normed), _ptr(out), _ptr(scales))
+    return out, scales, residual_out
+
+
+def rmsnorm_mxfp8(x, weight, residual=None, eps: float = 1e-6, out=None, scales=None, residual_out=None, normed=None):
+    """rmsnorm() with MXFP8 output; returns (codes uint8 [T, H], E8M0 scale bytes
+    uint8 [T, H/32], residual_out).  `normed` as in rmsnorm_fp8().  See
+    moe_rmsnorm_mxfp8 in include/moe_glue.h."""
+    torch = _torch()
+    T, H, residual_out = _norm_args(x, weight, residual, residual_out, normed, "normed")
+    if H % 32 != 0:
+        raise MoEGlueArgumentError(2, f"H={H} is not a multiple of the 32-column block")
+    if out is None:
+        out = torch.empty((T, H), dtype=torch.uint8, device=x.device)
+    else:
+        _check_shape("out", out, torch.uint8, (T, H), x.device)
+    if scales is None:
+        scales = torch.empty((T, H // 32), dtype=torch.uint8, device=x.device)
+    else:
+        _check_shape("scales", scales, torch.uint8, (T, H // 32), x.device)
+    _enqueue("moe_rmsnorm_mxfp8", x.device, _ptr(x), _ptr(residual), _ptr(weight), T, H, eps, _ptr(residual_out),
+             _ptr(normed), _ptr(out), _ptr(scales))
+    return out, scales, residual_out
+
+
+def decode_layer_workspace_bytes(T: int, E: int, k: int, I: int) -> int:
+    return int(load().moe_decode_layer_workspace_bytes(T, E, k, I))
+
+
+def alloc_decode_outputs(T: int, E: int, k: int, H: int, I: int, device) -> dict:
+    """Device buffers for decode_layer() and decode_layer_mxfp4(): ids, weights, out, workspace."""
+    torch = _torch()
+    return {
+        "topk_ids": torch.empty((T, k), dtype=torch.int32, device=device),
+        "topk_weights": torch.empty((T, k), dtype=torch.float32, device=device),
+        "out": torch.empty((T, H), dtype=torch.bfloat16, device=device),
+        "workspace": torch.empty((max(16, decode_layer_workspace_bytes(T, E, k, I)),), dtype=torch.uint8,
+                                 device=device),
+    }
+
+
+def _decode_args(logits, k: int, x, w_gate_up, w_down, bias, out, mx: bool):
+    """Checks shared by the two layers; returns (T, E, H, I, out)."""
+    torch = _torch()
+    _need_gpu("logits", logits, torch.float32, 2)
+    _need_gpu("x", x, torch.bfloat16, 2)
+    T, E = logits.shape
+    H = x.shape[1]
+    dev = x.device
+    if x.shape[0] != T:
+        raise MoEGlueArgumentError(2, f"x has {x.shape[0]} rows, logits has T={T}")
+    _same_device([("logits", logits), ("bias", bias)], dev)
+    _check_bias(bias, E)
+    dtype = torch.uint8 if mx else torch.bfloat16
+    _need_gpu("w_gate_up", w_gate_up, dtype, 3)
+    I = w_gate_up.shape[1] // 2
+    pack = 2 if mx else 1
+    if mx and (H % 32 != 0 or I % 32 != 0):
+        raise MoEGlueArgumentError(2, f"H={H} and I={I} must be multiples of the 32-column block")
+    _check_shape("w_gate_up", w_gate_up, dtype, (E, 2 * I, H // pack), dev)
+    _check_shape("w_down", w_down, dtype, (E, H, I // pack), dev)
+    if out is None:
+        if not 0 < k <= min(E, K_MAX):
+            raise MoEGlueArgumentError(2, f"k={k} must be in [1, {min(E, K_MAX)}]")
+        out = alloc_decode_outputs(T, E, k, H, I, dev)
+    else:
+        _check_shape("topk_ids", out.get("topk_ids"), torch.int32, (T, k), dev)
+        _check_shape("topk_weights", out.get("topk_weights"), torch.float32, (T, k), dev)
+        _check_shape("out", out.get("out"), torch.bfloat16, (T, H), dev)
+        ws = out.get("workspace")
+        _need_gpu("workspace", ws, torch.uint8)
+        _same_device([("workspace", ws)], dev)
+    return T, E, H, I, out
+
+
+def decode_layer(logits, k: int, x, w_gate_up, w_down, bias=None, out: dict | None = None) -> dict:
+    """The whole layer for T <= DECODE_T_MAX tokens, routing and experts, in two
+    launches: x [T, H], w_gate_up bf16 [E, 2I, H] (gate rows, then up rows),
+    w_down bf16 [E, H, I].  Returns "topk_ids", "topk_weights", "out" [T, H] and
+    the workspace.  See moe_decode_layer in include/moe_glue.h."""
+    T, E, H, I, out = _decode_args(logits, k, x, w_gate_up, w_down, bias, out, False)
+    ws = out["workspace"]
+    _enqueue("moe_decode_layer", x.device, _ptr(logits), _ptr(bias), T, E, k, _ptr(x), H, _ptr(w_gate_up),
+             _ptr(w_down), I, _ptr(out["topk_ids"]), _ptr(out["topk_weights"]), _ptr(out["out"]), _ptr(ws),
+             ws.numel())
+    return out
+
+
+def decode_layer_mxfp4(logits, k: int, x, w_gate_up, s_gate_up, w_down, s_down, bias=None,
+                       out: dict | None = None) -> dict:
+    """decode_layer() on MXFP4 expert weights: codes uint8 [E, 2I, H/2] and
+    [E, H, I/2] (lower column in the low four bits), E8M0 scale bytes uint8
+    [E, 2I, H/32] and [E, H, I/32].  See moe_decode_layer_mxfp4 in
+    include/moe_glue.h."""
+    u8 = _torch().uint8
+    T, E, H, I, out = _decode_args(logits, k, x, w_gate_up, w_down, bias, out, True)
+    _check_shape("s_gate_up", s_gate_up, u8, (E, 2 * I, H // 32), x.device)
+    _check_shape("s_down", s_down, u8, (E, H, I // 32), x.device)
+    ws = out["workspace"]
+    _enqueue("moe_decode_layer_mxfp4", x.device, _ptr(logits), _ptr(bias), T, E, k, _ptr(x), H, _ptr(w_gate_up),
+             _ptr(s_gate_up), _ptr(w_down), _ptr(s_down), I, _ptr(out["topk_ids"]), _ptr(out["topk_weights"]),
+             _ptr(out["out"]), _ptr(ws), ws.numel())
+    return out
+
+
+def linear_mxfp4(x, w, scales, out=None):
+    """y = x W^T for T <= DECODE_T_MAX tokens and MXFP4 weights: codes uint8
+    [N, K/2], E8M0 scale bytes uint8 [N, K/32]; returns bf16 [T, N].  See
+    moe_linear_mxfp4 in include/moe_glue.h."""
+    torch = _torch()
+    _need_gpu("x", x, torch.bfloat16, 2)
+    T, K = x.shape
+    if K % 32 != 0:
+        raise MoEGlueArgumentError(2, f"K={K} is not a multiple of the 32-column block")
+    _need_gpu("w", w, torch.uint8, 2)
+    N = w.shape[0]
+    _check_shape("w", w, torch.uint8, (N, K // 2), x.device)
+    _check_shape("scales", scales, torch.uint8, (N, K // 32), x.device)
+    if out is None:
+        out = torch.empty((T, N), dtype=torch.bfloat16, device=x.device)
+    else:
+        _check_shape("out", out, torch.bfloat16, (T, N), x.device)
+    _enqueue("moe_linear_mxfp4", x.device, _ptr(x), T, K, _ptr(w), _ptr(scales), N, _ptr(out))
     return out
 
 

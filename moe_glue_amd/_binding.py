@@ -17,11 +17,15 @@ MOE_OK, MOE_ERR_NULL, MOE_ERR_SHAPE, MOE_ERR_ALIGN, MOE_ERR_UNSUPPORTED, MOE_ERR
 E_MAX = 512
 K_MAX = 16
 PAD_MAX = 4096
+NORM_H_MAX = 65536
+DECODE_T_MAX = 64
 
 EXPORTED = ("moe_route_workspace_bytes", "moe_route", "moe_route_padded_rows", "moe_route_padded",
             "moe_expand_rows", "moe_expand_rows_fp8", "moe_expand_rows_mxfp8", "moe_route_expand", "moe_route_expand_padded",
             "moe_route_expand_fp8", "moe_route_expand_mxfp8", "moe_noalloc_scratch_bytes", "moe_route_expand_noalloc",
-            "moe_swiglu", "moe_combine", "moe_copy_probe", "moe_mix_probe",
+            "moe_swiglu", "moe_combine", "moe_rmsnorm", "moe_rmsnorm_fp8", "moe_rmsnorm_mxfp8",
+            "moe_decode_layer_workspace_bytes", "moe_decode_layer", "moe_decode_layer_mxfp4", "moe_linear_mxfp4",
+            "moe_copy_probe", "moe_mix_probe",
             "moe_status_string", "moe_last_error")
 # include/moe_glue_testing.h
 TESTING_EXPORTED = ("moe_testing_force",)
@@ -97,6 +101,23 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.moe_swiglu.argtypes = [_vp, _i32, _i32, _vp, _vp]
     lib.moe_combine.restype = ctypes.c_int
     lib.moe_combine.argtypes = [_vp, _vp, _vp, _i32, _i32, _i32, _vp, _vp]
+    _f32 = ctypes.c_float
+    lib.moe_rmsnorm.restype = ctypes.c_int
+    lib.moe_rmsnorm.argtypes = [_vp, _vp, _vp, _i32, _i32, _f32, _vp, _vp, _vp]
+    lib.moe_rmsnorm_fp8.restype = ctypes.c_int
+    lib.moe_rmsnorm_fp8.argtypes = [_vp, _vp, _vp, _i32, _i32, _f32, _i32, _vp, _vp, _vp, _vp, _vp]
+    lib.moe_rmsnorm_mxfp8.restype = ctypes.c_int
+    lib.moe_rmsnorm_mxfp8.argtypes = [_vp, _vp, _vp, _i32, _i32, _f32, _vp, _vp, _vp, _vp, _vp]
+    lib.moe_decode_layer_workspace_bytes.restype = ctypes.c_size_t
+    lib.moe_decode_layer_workspace_bytes.argtypes = [_i32, _i32, _i32, _i32]
+    lib.moe_decode_layer.restype = ctypes.c_int
+    lib.moe_decode_layer.argtypes = [_vp, _vp, _i32, _i32, _i32, _vp, _i32, _vp, _vp, _i32, _vp, _vp, _vp, _vp,
+                                     ctypes.c_size_t, _vp]
+    lib.moe_decode_layer_mxfp4.restype = ctypes.c_int
+    lib.moe_decode_layer_mxfp4.argtypes = [_vp, _vp, _i32, _i32, _i32, _vp, _i32, _vp, _vp, _vp, _vp, _i32, _vp, _vp,
+                                           _vp, _vp, ctypes.c_size_t, _vp]
+    lib.moe_linear_mxfp4.restype = ctypes.c_int
+    lib.moe_linear_mxfp4.argtypes = [_vp, _i32, _i32, _vp, _vp, _i32, _vp, _vp]
     lib.moe_copy_probe.restype = ctypes.c_int
     lib.moe_copy_probe.argtypes = [_vp, _vp, ctypes.c_size_t, _vp]
     lib.moe_mix_probe.restype = ctypes.c_int

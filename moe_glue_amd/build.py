@@ -20,8 +20,8 @@ LIB = os.path.join(LIBDIR, "libmoe_glue.so")
 BUILD = os.path.join(ROOT, "_build")
 
 SOURCES = ["api.cpp", "route.hip", "dispatch.hip", "expand.hip", "quant.hip", "swiglu.hip", "combine.hip",
-           "probe.hip", "noalloc.hip", "place_expand.hip"]
-HEADERS = ["device_common.h", "kernels.h", "route_common.h", "fp8_common.h", "place_copy.h"]
+           "probe.hip", "noalloc.hip", "place_expand.hip", "norm.hip", "decode_layer.hip", "linear.hip"]
+HEADERS = ["device_common.h", "kernels.h", "route_common.h", "fp8_common.h", "place_copy.h", "mfma_rows.h"]
 ARCH = "gfx950"
 
 # -packed-fp32-ops off: hipcc would otherwise form v_pk_{add,mul,fma}_f32 from

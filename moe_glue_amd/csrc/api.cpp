@@ -5,6 +5,7 @@
 
 #include <hip/hip_runtime_api.h>
 
+#include <cfloat>
 #include <cstdarg>
 #include <cstdio>
 #include <atomic>
@@ -544,6 +545,155 @@ moe_status moe_combine(const uint16_t* y, const float* topk_weights, const int32
     if (!aligned4(topk_weights)) return fail(MOE_ERR_ALIGN, "moe_combine: topk_weights must be 4-byte aligned");
     return from_hip(moe::launch_combine(y, topk_weights, dest_of_src, T, H, k, out, static_cast<hipStream_t>(stream)),
                     "moe_combine launch");
+}
+
+}  // extern "C"
+
+namespace {
+
+bool aligned2(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 1u) == 0; }
+bool aligned8(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 7u) == 0; }
+
+// Checks shared by the three norms; `codes` and `scales` unless the output is
+// bf16 alone.
+moe_status check_norm_args(const char* fn, const moe::NormArgs& a, bool quantised) {
+    moe_status s = check_rows(fn, a.T, a.H, "H");
+    if (s != MOE_OK) return s;
+    if (a.H > MOE_NORM_H_MAX) return fail(MOE_ERR_UNSUPPORTED, "%s: H=%d exceeds %d", fn, a.H, MOE_NORM_H_MAX);
+    if (!(a.eps >= FLT_MIN && a.eps <= FLT_MAX))  // false for NaN
+        return fail(MOE_ERR_UNSUPPORTED, "%s: eps=%g must be finite and a positive normal fp32", fn, (double)a.eps);
+    if (quantised && !a.mx && (a.group < 8 || a.group > 512 || (a.group & (a.group - 1)) != 0))
+        return fail(MOE_ERR_UNSUPPORTED, "%s: group=%d must be a power of two in [8, 512]", fn, a.group);
+    if (quantised && a.H % a.group != 0)
+        return fail(MOE_ERR_SHAPE, "%s: H=%d is not a multiple of the group of %d columns", fn, a.H, a.group);
+    if (a.T == 0) return MOE_OK;
+    if (!a.x || !a.weight || (quantised ? !a.codes || !a.scales : !a.out))
+        return fail(MOE_ERR_NULL, "%s: NULL tensor pointer", fn);
+    if (a.residual_out && !a.residual) return fail(MOE_ERR_NULL, "%s: residual_out without residual", fn);
+    if (!aligned16(a.x) || !aligned16(a.residual) || !aligned16(a.weight) || !aligned16(a.residual_out) ||
+        !aligned16(a.out))
+        return fail(MOE_ERR_ALIGN, "%s: bf16 tensors must be 16-byte aligned", fn);
+    if (quantised && (!aligned8(a.codes) || (!a.mx && !aligned4(a.scales))))
+        return fail(MOE_ERR_ALIGN, "%s: codes must be 8-byte and fp32 scales 4-byte aligned", fn);
+    return MOE_OK;
+}
+
+moe_status norm_impl(const char* fn, const moe::NormArgs& a, bool quantised, void* stream) {
+    const moe_status s = check_norm_args(fn, a, quantised);
+    if (s != MOE_OK) return s;
+    if (a.T == 0) return ok();
+    return from_hip(moe::launch_rmsnorm(a, static_cast<hipStream_t>(stream)), fn);
+}
+
+// Widths of the few-token products: rows of weights hold whole 16-byte vectors
+// (bf16) or whole 32-column blocks (MXFP4).
+moe_status check_decode_width(const char* fn, const char* name, int32_t width, bool mx) {
+    if (width < 1) return fail(MOE_ERR_SHAPE, "%s: %s=%d must be >= 1", fn, name, width);
+    if (mx && width % 32 != 0)
+        return fail(MOE_ERR_SHAPE, "%s: %s=%d is not a multiple of the 32-column block", fn, name, width);
+    if (!mx && width % 8 != 0)
+        return fail(MOE_ERR_ALIGN, "%s: %s=%d: bf16 rows must be a multiple of 16 bytes (%s %% 8 == 0)", fn, name,
+                    width, name);
+    if (width > MOE_DECODE_WIDTH_MAX)
+        return fail(MOE_ERR_UNSUPPORTED, "%s: %s=%d exceeds %d", fn, name, width, MOE_DECODE_WIDTH_MAX);
+    return MOE_OK;
+}
+
+moe_status check_decode_sizes(const char* fn, int32_t T, int32_t E, int32_t k) {
+    const moe_status s = check_route_sizes(T, E, k);
+    if (s != MOE_OK) return s;
+    if (T > MOE_DECODE_T_MAX) return fail(MOE_ERR_UNSUPPORTED, "%s: T=%d exceeds %d", fn, T, MOE_DECODE_T_MAX);
+    return MOE_OK;
+}
+
+moe_status decode_layer_impl(const char* fn, const moe::DecodeLayerArgs& a, bool mx, size_t workspace_bytes,
+                             void* stream) {
+    moe_status s = check_decode_sizes(fn, a.T, a.E, a.k);
+    if (s != MOE_OK) return s;
+    if ((s = check_decode_width(fn, "H", a.H, mx)) != MOE_OK) return s;
+    if ((s = check_decode_width(fn, "I", a.I, mx)) != MOE_OK) return s;
+    if (a.T == 0) return ok();
+    if (!a.logits || !a.x || !a.w_gate_up || !a.w_down || !a.topk_ids || !a.topk_weights || !a.out ||
+        (mx && (!a.s_gate_up || !a.s_down)))
+        return fail(MOE_ERR_NULL, "%s: NULL tensor pointer", fn);
+    if (!aligned4(a.logits) || !aligned4(a.bias) || !aligned4(a.topk_ids) || !aligned4(a.topk_weights))
+        return fail(MOE_ERR_ALIGN, "%s: logits, bias, ids and weights must be 4-byte aligned", fn);
+    if (!aligned16(a.x) || !aligned16(a.w_gate_up) || !aligned16(a.w_down) || !aligned16(a.out))
+        return fail(MOE_ERR_ALIGN, "%s: x, the expert weights and out must be 16-byte aligned", fn);
+    const size_t need = moe::decode_layer_workspace_bytes(a.T, a.k, a.I);
+    if (a.workspace == nullptr || workspace_bytes < need)
+        return fail(MOE_ERR_WORKSPACE, "%s: workspace of %zu bytes needed, %zu given%s", fn, need, workspace_bytes,
+                    a.workspace ? "" : " (NULL)");
+    if (!aligned16(a.workspace)) return fail(MOE_ERR_WORKSPACE, "%s: workspace must be 16-byte aligned", fn);
+    return from_hip(moe::launch_decode_layer(a, static_cast<hipStream_t>(stream)), fn);
+}
+
+}  // namespace
+
+extern "C" {
+
+moe_status moe_rmsnorm(const uint16_t* x, const uint16_t* residual, const uint16_t* weight, int32_t T, int32_t H,
+                       float eps, uint16_t* residual_out, uint16_t* out, void* stream) {
+    return norm_impl("moe_rmsnorm", {x, residual, weight, T, H, eps, residual_out, out, nullptr, nullptr, 8, false},
+                     false, stream);
+}
+
+moe_status moe_rmsnorm_fp8(const uint16_t* x, const uint16_t* residual, const uint16_t* weight, int32_t T, int32_t H,
+                           float eps, int32_t group, uint16_t* residual_out, uint16_t* out, uint8_t* codes,
+                           float* scales, void* stream) {
+    return norm_impl("moe_rmsnorm_fp8",
+                     {x, residual, weight, T, H, eps, residual_out, out, codes, scales, group, false}, true, stream);
+}
+
+moe_status moe_rmsnorm_mxfp8(const uint16_t* x, const uint16_t* residual, const uint16_t* weight, int32_t T, int32_t H,
+                             float eps, uint16_t* residual_out, uint16_t* out, uint8_t* codes, uint8_t* scales,
+                             void* stream) {
+    return norm_impl("moe_rmsnorm_mxfp8", {x, residual, weight, T, H, eps, residual_out, out, codes, scales, 32, true},
+                     true, stream);
+}
+
+size_t moe_decode_layer_workspace_bytes(int32_t T, int32_t E, int32_t k, int32_t I) {
+    const char* fn = "moe_decode_layer_workspace_bytes";
+    if (check_decode_sizes(fn, T, E, k) != MOE_OK || check_decode_width(fn, "I", I, false) != MOE_OK) return 0;
+    return moe::decode_layer_workspace_bytes(T, k, I);
+}
+
+moe_status moe_decode_layer(const float* logits, const float* bias, int32_t T, int32_t E, int32_t k,
+                            const uint16_t* x, int32_t H, const uint16_t* w_gate_up, const uint16_t* w_down,
+                            int32_t I, int32_t* topk_ids, float* topk_weights, uint16_t* out, void* workspace,
+                            size_t workspace_bytes, void* stream) {
+    return decode_layer_impl("moe_decode_layer",
+                             {logits, bias, T, E, k, x, H, w_gate_up, nullptr, w_down, nullptr, I, topk_ids,
+                              topk_weights, out, workspace},
+                             false, workspace_bytes, stream);
+}
+
+moe_status moe_decode_layer_mxfp4(const float* logits, const float* bias, int32_t T, int32_t E, int32_t k,
+                                  const uint16_t* x, int32_t H, const uint8_t* w_gate_up, const uint8_t* s_gate_up,
+                                  const uint8_t* w_down, const uint8_t* s_down, int32_t I, int32_t* topk_ids,
+                                  float* topk_weights, uint16_t* out, void* workspace, size_t workspace_bytes,
+                                  void* stream) {
+    return decode_layer_impl("moe_decode_layer_mxfp4",
+                             {logits, bias, T, E, k, x, H, w_gate_up, s_gate_up, w_down, s_down, I, topk_ids,
+                              topk_weights, out, workspace},
+                             true, workspace_bytes, stream);
+}
+
+moe_status moe_linear_mxfp4(const uint16_t* x, int32_t T, int32_t K, const uint8_t* w, const uint8_t* scales,
+                            int32_t N, uint16_t* y, void* stream) {
+    const char* fn = "moe_linear_mxfp4";
+    if (T < 0) return fail(MOE_ERR_SHAPE, "%s: T=%d is negative", fn, T);
+    if (T > MOE_DECODE_T_MAX) return fail(MOE_ERR_UNSUPPORTED, "%s: T=%d exceeds %d", fn, T, MOE_DECODE_T_MAX);
+    const moe_status s = check_decode_width(fn, "K", K, true);
+    if (s != MOE_OK) return s;
+    if (N < 1) return fail(MOE_ERR_SHAPE, "%s: N=%d must be >= 1", fn, N);
+    if (N > MOE_DECODE_WIDTH_MAX) return fail(MOE_ERR_UNSUPPORTED, "%s: N=%d exceeds %d", fn, N, MOE_DECODE_WIDTH_MAX);
+    if (T == 0) return ok();
+    if (!x || !w || !scales || !y) return fail(MOE_ERR_NULL, "%s: NULL tensor pointer", fn);
+    if (!aligned16(x) || !aligned16(w) || !aligned2(y))
+        return fail(MOE_ERR_ALIGN, "%s: x and w must be 16-byte and y 2-byte aligned", fn);
+    return from_hip(moe::launch_linear_mxfp4(x, T, K, w, scales, N, y, static_cast<hipStream_t>(stream)),
+                    "moe_linear_mxfp4 launch");
 }
 
 int moe_testing_force(int route_variant, int expand_order, int workgroups_per_group) {

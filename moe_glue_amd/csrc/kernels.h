@@ -202,6 +202,52 @@ hipError_t launch_copy_probe(const void* src, void* dst, size_t bytes, hipStream
 hipError_t launch_mix_probe(const void* src, void* dst, uint32_t cycles, uint32_t reads, uint32_t writes,
                             int vectors_per_lane, int threads, hipStream_t stream);
 
+// ------------------------------------------------------------------- norm
+// Widest row: 16 waves of 8 16-byte vectors a lane.
+constexpr int kNormMaxWidth = MOE_NORM_H_MAX;
+struct NormArgs {
+    const void* x;         // bf16 [T, H]
+    const void* residual;  // bf16 [T, H] or null
+    const void* weight;    // bf16 [H]
+    int T, H;
+    float eps;
+    void* residual_out;  // bf16 [T, H] or null
+    void* out;           // bf16 [T, H] or null
+    void* codes;         // E4M3 [T, H] or null
+    void* scales;        // fp32 [T, H/group], or E8M0 [T, H/32] with mx
+    int group;           // columns per scale (32 with mx)
+    bool mx;
+};
+hipError_t launch_rmsnorm(const NormArgs& a, hipStream_t stream);
+
+// ------------------------------------------------------- few-token products
+constexpr int kDecodeLayerMaxTokens = MOE_DECODE_T_MAX;
+// Front part of the few-token layer's workspace: the routing tables its first
+// launch writes for its second; the activations [T*k, I] bf16 follow.
+constexpr size_t kDecodeLayerTableBytes = 8448;
+inline size_t decode_layer_workspace_bytes(int T, int k, int I) {
+    return kDecodeLayerTableBytes + (size_t)T * k * I * 2;
+}
+struct DecodeLayerArgs {
+    const float* logits;
+    const float* bias;
+    int T, E, k;
+    const void* x;  // bf16 [T, H]
+    int H;
+    const void* w_gate_up;     // [E, 2I, H] bf16, or E2M1 codes [E, 2I, H/2] with scales
+    const uint8_t* s_gate_up;  // E8M0 [E, 2I, H/32], or null (bf16 weights)
+    const void* w_down;        // [E, H, I]
+    const uint8_t* s_down;
+    int I;
+    int32_t* topk_ids;
+    float* topk_weights;
+    void* out;  // bf16 [T, H]
+    void* workspace;
+};
+hipError_t launch_decode_layer(const DecodeLayerArgs& a, hipStream_t stream);
+hipError_t launch_linear_mxfp4(const void* x, int T, int K, const uint8_t* w, const uint8_t* scales, int N, void* y,
+                               hipStream_t stream);
+
 // ------------------------------------------------------- built-in scratch
 // Bytes of the file-scope device array behind moe_route_expand_noalloc.
 constexpr size_t kNoAllocScratchBytes = (size_t)MOE_NOALLOC_SCRATCH_BYTES;
