@@ -18,12 +18,9 @@
 // product.  Workgroup 0 writes the ids, the weights and the tables that launch
 // 2 reads.
 //
-// Launch 2.  A workgroup owns 4 output columns, for every token, so the sum
-// over experts needs no atomics and no third launch.  Four rows are a quarter
-// of an MFMA tile: a tile takes the 4 rows of 4 experts, whose tokens are
-// consecutive p, and the lane that holds column p and the quarter of its own
-// expert has the 4 outputs; the other quarters are products nobody asked for.
-// The waves of a workgroup deal these units, and split K when there are few.
+// Launch 2.  A workgroup owns a few output columns (4 rows of w_down, 8 with
+// MXFP4) for every token, so the sum over experts needs no atomics and no third
+// launch.  Its waves deal the active experts, and split K when there are few.
 // fp32 y meets in LDS and is summed over j in order, so the same call always
 // gives the same bits.
 #include "kernels.h"
@@ -56,61 +53,67 @@ __device__ __forceinline__ float silu_mul(float g, float u) {
     return g * __builtin_amdgcn_rcpf(1.0f + e) * u;
 }
 
-template <class W>
-__device__ __forceinline__ WeightRow weight_row(const uint8_t* w, const uint8_t* scales, size_t row, int K) {
-    return {w + row * W::row_bytes(K), scales + row * W::row_scales(K)};
-}
+// Row tiles of an item: 16 gate rows, then their 16 up rows, 4 to a tile.
+constexpr int kItemTiles = 8;
 
-// Partial sums of one 16x16 tile pair: [wave][gate or up][lane].
-struct GateUpShared {
-    f32x4 part[kWaves][2][kWave];
-};
+// One wave's sums of an item: [row tile][row of the tile * 4 + column].
+template <int NT>
+using ItemSums = float[NT][kItemTiles][16];
 
+// Columns c0 .. c0 + 4 NT - 1 of an item.  `flip` alternates between the two
+// halves of `sums`, so one barrier an item is enough: a wave that writes the
+// half used two items ago has passed the barrier after it was read.
 template <class W, int NT>
-__device__ __forceinline__ void gate_up_item(const uint16_t* __restrict__ x, int H, const uint8_t* __restrict__ w,
-                                             const uint8_t* __restrict__ sc, int I, int e, int i0,
-                                             unsigned long long mask, int m, int c0, size_t p0,
-                                             uint16_t* __restrict__ act, GateUpShared& sh) {
+__device__ __forceinline__ void gate_up_item(const uint8_t* x, int H, const uint8_t* w, const uint8_t* sc, int I,
+                                             uint32_t e, uint32_t i0, unsigned long long mask, int m, int c0,
+                                             uint32_t p0, uint16_t* __restrict__ act, ItemSums<NT>* sums) {
     const int lane = (int)(threadIdx.x % kWave);
-    const int wave = (int)(threadIdx.x / kWave);
-    const size_t gate = (size_t)e * 2 * I + min(i0 + lane % 16, I - 1);
-    const WeightRow rows[2] = {weight_row<W>(w, sc, gate, H), weight_row<W>(w, sc, gate + I, H)};
-    const uint16_t* cols[NT];
+    const int wave = wave_index();
+    const size_t first = (size_t)e * 2 * I + i0;
+    const WeightBase gate{w + uniform_offset(first * W::row_bytes(H)), sc + uniform_offset(first * W::row_scales(H))};
+    const WeightBase up{gate.w + (size_t)I * W::row_bytes(H), gate.scales + (size_t)I * W::row_scales(H)};
+    WeightBase base[kItemTiles];
+    uint32_t row[kItemTiles], col[NT];
 #pragma unroll
-    for (int c = 0; c < NT; ++c) {
-        const int t = select_bit(mask, min(c0 + c * 16 + lane % 16, m - 1));
-        cols[c] = x + (size_t)t * H;
+    for (int r = 0; r < kItemTiles; ++r) {
+        base[r] = r < kItemTiles / 2 ? gate : up;
+        row[r] = min((uint32_t)(r % (kItemTiles / 2) * 4 + lane % 16 / 4), (uint32_t)I - 1 - i0);
     }
-    f32x4 acc[2][NT];
 #pragma unroll
-    for (int r = 0; r < 2; ++r)
+    for (int c = 0; c < NT; ++c)
+        col[c] = (uint32_t)select_bit(mask, min(c0 + c * 4 + lane % 16 / 4, m - 1)) * (uint32_t)H * 2;
+    f32x4 acc[kItemTiles][NT];
+#pragma unroll
+    for (int r = 0; r < kItemTiles; ++r)
 #pragma unroll
         for (int c = 0; c < NT; ++c) acc[r][c] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-    const int steps = (H + W::STEP - 1) / W::STEP;
-    multiply_rows<W, 2, NT>(rows, cols, H, steps * wave / kWaves, steps * (wave + 1) / kWaves, acc);
+    const int steps = (H + kStep - 1) / kStep;
+    multiply_rows<W, kItemTiles, NT, (NT == 1 ? 2 : 1)>(base, row, x, col, H, steps * wave / kWaves, steps * (wave + 1) / kWaves, acc);
 #pragma unroll
-    for (int c = 0; c < NT; ++c) {
-        __syncthreads();  // the last tile's sums are read
-        sh.part[wave][0][lane] = acc[0][c];
-        sh.part[wave][1][lane] = acc[1][c];
-        __syncthreads();
-        if (threadIdx.x < 256) {
-            const int l = (int)threadIdx.x / 4, v = (int)threadIdx.x % 4;
-            float g = 0.0f, u = 0.0f;
+    for (int c = 0; c < NT; ++c)
 #pragma unroll
-            for (int k = 0; k < kWaves; ++k) {
-                g += sh.part[k][0][l][v];
-                u += sh.part[k][1][l][v];
-            }
-            const int col = c0 + c * 16 + l % 16, i = i0 + l / 16 * 4 + v;
-            if (col < m && i < I)
-                act[(p0 + col) * I + i] = (uint16_t)(pack_bf16x2(silu_mul(g, u), 0.0f) & 0xFFFFu);
+        for (int r = 0; r < kItemTiles; ++r) {
+            const float v = diagonal_sum(acc[r][c]);
+            if (lane % 4 == r % 4) sums[wave][c][r][lane / 16 * 4 + lane % 16 / 4] = v;
         }
+    __syncthreads();
+    for (int o = (int)threadIdx.x; o < NT * 64; o += kThreads) {
+        const int c = o / 64, r = o / 16 % 4, at = o % 16;
+        float g = 0.0f, u = 0.0f;
+#pragma unroll
+        for (int k = 0; k < kWaves; ++k) {
+            g += sums[k][c][r][at];
+            u += sums[k][c][r + kItemTiles / 2][at];
+        }
+        const int column = c0 + c * 4 + at % 4;
+        const uint32_t i = i0 + r * 4 + at / 4;
+        if (column < m && i < (uint32_t)I)
+            act[(size_t)(p0 + column) * I + i] = (uint16_t)(pack_bf16x2(silu_mul(g, u), 0.0f) & 0xFFFFu);
     }
 }
 
 template <class W, int G, int V>
-__global__ __launch_bounds__(kThreads) void decode_gate_up_kernel(
+__global__ __launch_bounds__(kThreads, 4) void decode_gate_up_kernel(
     const float* __restrict__ logits, const float* __restrict__ bias, int T, int E, int k,
     const uint16_t* __restrict__ x, int H, const uint8_t* __restrict__ w, const uint8_t* __restrict__ sc, int I,
     int32_t* __restrict__ topk_ids, float* __restrict__ topk_weights, Tables* __restrict__ tables,
@@ -122,10 +125,10 @@ __global__ __launch_bounds__(kThreads) void decode_gate_up_kernel(
     __shared__ int32_t s_first[kEMax + 1];
     __shared__ int32_t s_off[kEMax];  // first p by expert
     __shared__ int32_t s_n;
-    __shared__ GateUpShared sh;
+    __shared__ float s_sums[2][kWaves * 2 * kItemTiles * 16];  // two halves for up to 2 column tiles
 
     const int lane = (int)(threadIdx.x % kWave);
-    const int wave = (int)(threadIdx.x / kWave);
+    const int wave = wave_index();
     const bool writer = blockIdx.x == 0;
     for (int e = (int)threadIdx.x; e < E; e += kThreads) s_mask[e] = 0ull;
     __syncthreads();
@@ -173,45 +176,70 @@ __global__ __launch_bounds__(kThreads) void decode_gate_up_kernel(
         }
     }
     const int tiles = (I + 15) / 16;
+    int half = 0;
     for (int it = (int)blockIdx.x; it < n * tiles; it += (int)gridDim.x) {
         const int a = it / tiles;
-        const int e = s_expert[a];
+        const uint32_t e = uniform((uint32_t)s_expert[a]);
         const unsigned long long mask = s_mask[e];
-        const int m = __popcll(mask);
-        const int i0 = (it - a * tiles) * 16;
-        const size_t p0 = (size_t)s_first[a];
-        for (int c0 = 0; c0 < m; c0 += 32) {
-            if (m - c0 <= 16)
-                gate_up_item<W, 1>(x, H, w, sc, I, e, i0, mask, m, c0, p0, act, sh);
+        const int m = (int)uniform((uint32_t)__popcll(mask));
+        const uint32_t i0 = (uint32_t)(it - a * tiles) * 16;
+        const uint32_t p0 = uniform((uint32_t)s_first[a]);
+        const uint8_t* xb = reinterpret_cast<const uint8_t*>(x);
+        for (int c0 = 0; c0 < m; c0 += 8) {
+            if (m - c0 <= 4)
+                gate_up_item<W, 1>(xb, H, w, sc, I, e, i0, mask, m, c0, p0, act,
+                                   reinterpret_cast<ItemSums<1>*>(s_sums[half]));
             else
-                gate_up_item<W, 2>(x, H, w, sc, I, e, i0, mask, m, c0, p0, act, sh);
+                gate_up_item<W, 2>(xb, H, w, sc, I, e, i0, mask, m, c0, p0, act,
+                                   reinterpret_cast<ItemSums<2>*>(s_sums[half]));
+            half ^= 1;
         }
     }
 }
 
-// Most y entries of a workgroup: pairs times K parts (see parts()).
-constexpr int kMaxY = 3072;
+// Output columns of a workgroup of launch 2, in tiles of 4 rows of w_down.
+template <class W>
+constexpr int kDownTiles = 1;
+template <>
+constexpr int kDownTiles<Mxfp4Weights> = 2;
 
-// K parts of a unit (4 experts) by the number of units: enough that the eight
-// waves all have work.  Up to 4 experts hold at most 256 pairs, 12 at most
-// 768, and more at most 1024 (k is at most the number of active experts).
-__device__ __forceinline__ int k_parts(int units) { return units >= 8 ? 1 : units >= 4 ? 2 : units >= 2 ? 4 : 8; }
+constexpr int kMaxY = kMaxSlots;  // y entries of a workgroup: pairs times K parts
+
+// K parts of an expert's rows: enough that the eight waves have two tasks each,
+// as long as y holds them.  One part always fits: there are at most kMaxSlots
+// pairs.
+__device__ __forceinline__ int k_parts(int n, int pairs) {
+    int parts = 8;
+    while (parts > 1 && (n * parts > 16 || pairs * parts > kMaxY)) parts /= 2;
+    return parts;
+}
 
 template <class W, int NT>
-__device__ __forceinline__ void down_columns(const WeightRow (&rows)[1], const uint16_t* __restrict__ act, int I,
-                                             int p0, int lo, int hi, int end, int s0, int s1, f32x4* y) {
+__device__ __forceinline__ void down_columns(const WeightBase& rows, int left, const uint8_t* act, int I, int p0,
+                                             int end, int s0, int s1, float* y) {
+    constexpr int RT = kDownTiles<W>;
     const int lane = (int)(threadIdx.x % kWave);
-    const uint16_t* cols[NT];
+    WeightBase base[RT];
+    uint32_t row[RT], col[NT];
+    f32x4 acc[RT][NT];
 #pragma unroll
-    for (int c = 0; c < NT; ++c) cols[c] = act + (size_t)min(p0 + c * 16 + lane % 16, end - 1) * I;
-    f32x4 acc[1][NT];
+    for (int r = 0; r < RT; ++r) {
+        base[r] = rows;
+        row[r] = (uint32_t)min(r * 4 + lane % 16 / 4, left - 1);
 #pragma unroll
-    for (int c = 0; c < NT; ++c) acc[0][c] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-    multiply_rows<W, 1, NT>(rows, cols, I, s0, s1, acc);
+        for (int c = 0; c < NT; ++c) acc[r][c] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    }
+#pragma unroll
+    for (int c = 0; c < NT; ++c) col[c] = (uint32_t)min(p0 + c * 4 + lane % 16 / 4, end - 1) * (uint32_t)I * 2;
+    multiply_rows<W, RT, NT, 4>(base, row, act, col, I, s0, s1, acc);
 #pragma unroll
     for (int c = 0; c < NT; ++c) {
-        const int p = p0 + c * 16 + lane % 16;
-        if (p >= lo && p < hi) y[p] = acc[0][c];  // this lane's quarter is the column's expert
+        const int p = p0 + c * 4 + lane % 16 / 4;
+#pragma unroll
+        for (int r = 0; r < RT; ++r) {
+            const float v = diagonal_sum(acc[r][c]);
+            if (lane % 4 == r && p < end) y[p * (4 * RT) + r * 4 + lane / 16] = v;
+        }
     }
 }
 
@@ -222,46 +250,43 @@ __global__ __launch_bounds__(kThreads) void decode_down_kernel(int T, int k, con
                                                                const uint16_t* __restrict__ act,
                                                                const float* __restrict__ topk_weights,
                                                                uint16_t* __restrict__ out) {
-    __shared__ f32x4 s_y[kMaxY];
+    constexpr int ROWS = 4 * kDownTiles<W>;
+    __shared__ float s_y[kMaxY * ROWS];  // [part][p][row]
     __shared__ float s_w[kMaxSlots];
     __shared__ int32_t s_dest[kMaxSlots];
-    const int lane = (int)(threadIdx.x % kWave);
-    const int wave = (int)(threadIdx.x / kWave);
-    const int h0 = (int)blockIdx.x * 4;
+    const int wave = wave_index();
+    const int h0 = (int)blockIdx.x * ROWS;
     const int n = tables->n;
     const int pairs = tables->first[n];
     for (int s = (int)threadIdx.x; s < T * k; s += kThreads) {
         s_w[s] = topk_weights[s];
         s_dest[s] = tables->dest[s];
     }
-    const int units = (n + 3) / 4;
-    const int parts = k_parts(units);
-    const int steps = (I + W::STEP - 1) / W::STEP;
-    for (int task = wave; task < units * parts; task += kWaves) {
-        const int u = task / parts, part = task - u * parts;
-        const int mine = min(4 * u + lane % 16 / 4, n - 1);  // the expert of the lane's weight row
-        const size_t row = (size_t)tables->expert[mine] * H + min(h0 + lane % 4, H - 1);
-        const WeightRow rows[1] = {weight_row<W>(w, sc, row, I)};
-        const int quarter = 4 * u + lane / 16;  // the expert of the lane's accumulators
-        const int lo = tables->first[min(quarter, n)], hi = tables->first[min(quarter + 1, n)];
-        const int begin = tables->first[4 * u], end = tables->first[min(4 * u + 4, n)];
+    const int parts = k_parts(n, pairs);
+    const int steps = (I + kStep - 1) / kStep;
+    const uint8_t* actb = reinterpret_cast<const uint8_t*>(act);
+    for (int task = wave; task < n * parts; task += kWaves) {
+        const int a = task / parts, part = task - a * parts;
+        const size_t row = (size_t)tables->expert[a] * H + h0;
+        const WeightBase rows{w + uniform_offset(row * W::row_bytes(I)), sc + uniform_offset(row * W::row_scales(I))};
+        const int begin = tables->first[a], end = tables->first[a + 1];
         const int s0 = steps * part / parts, s1 = steps * (part + 1) / parts;
-        f32x4* y = s_y + part * pairs;
-        for (int p0 = begin; p0 < end; p0 += 32) {
-            if (end - p0 <= 16)
-                down_columns<W, 1>(rows, act, I, p0, lo, hi, end, s0, s1, y);
+        float* y = s_y + part * pairs * ROWS;
+        for (int p0 = begin; p0 < end; p0 += 8) {
+            if (end - p0 <= 4)
+                down_columns<W, 1>(rows, H - h0, actb, I, p0, end, s0, s1, y);
             else
-                down_columns<W, 2>(rows, act, I, p0, lo, hi, end, s0, s1, y);
+                down_columns<W, 2>(rows, H - h0, actb, I, p0, end, s0, s1, y);
         }
     }
     __syncthreads();
-    for (int i = (int)threadIdx.x; i < T * 4; i += kThreads) {
-        const int t = i / 4, h = i % 4;
+    for (int i = (int)threadIdx.x; i < T * ROWS; i += kThreads) {
+        const int t = i / ROWS, h = i % ROWS;
         float sum = 0.0f;
         for (int j = 0; j < k; ++j) {
             const int s = t * k + j;
             float y = 0.0f;
-            for (int part = 0; part < parts; ++part) y += s_y[part * pairs + s_dest[s]][h];
+            for (int part = 0; part < parts; ++part) y += s_y[(part * pairs + s_dest[s]) * ROWS + h];
             sum = fmaf(s_w[s], y, sum);
         }
         if (h0 + h < H) out[(size_t)t * H + h0 + h] = (uint16_t)(pack_bf16x2(sum, 0.0f) & 0xFFFFu);
@@ -282,7 +307,7 @@ hipError_t launch_gv(const DecodeLayerArgs& a, hipStream_t stream) {
         a.topk_ids, a.topk_weights, tables, act);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
-    decode_down_kernel<W><<<(a.H + 3) / 4, kThreads, 0, stream>>>(
+    decode_down_kernel<W><<<(a.H + 4 * kDownTiles<W> - 1) / (4 * kDownTiles<W>), kThreads, 0, stream>>>(
         a.T, a.k, static_cast<const uint8_t*>(a.w_down), a.s_down, a.H, a.I, tables, act, a.topk_weights,
         static_cast<uint16_t*>(a.out));
     return hipGetLastError();

@@ -12,35 +12,49 @@ namespace {
 constexpr int kThreads = 512;
 constexpr int kWaves = kThreads / kWave;
 
+constexpr int kTiles = 4;  // row tiles of a workgroup: 16 rows of W
+
 template <int NT>
 __global__ __launch_bounds__(kThreads) void linear_mxfp4_kernel(const uint16_t* __restrict__ x, int T, int K,
                                                                 const uint8_t* __restrict__ w,
                                                                 const uint8_t* __restrict__ sc, int N,
                                                                 uint16_t* __restrict__ y) {
-    __shared__ f32x4 s_part[kWaves][NT][kWave];
+    using W = Mxfp4Weights;
+    __shared__ float s_sums[kWaves][NT][kTiles][16];
     const int lane = (int)(threadIdx.x % kWave);
-    const int wave = (int)(threadIdx.x / kWave);
-    const int n0 = (int)blockIdx.x * 16;
-    const size_t row = (size_t)min(n0 + lane % 16, N - 1);
-    const WeightRow rows[1] = {{w + row * Mxfp4Weights::row_bytes(K), sc + row * Mxfp4Weights::row_scales(K)}};
-    const uint16_t* cols[NT];
-    f32x4 acc[1][NT];
+    const int wave = wave_index();
+    const int n0 = (int)blockIdx.x * (4 * kTiles);
+    const int c0 = (int)blockIdx.y * (4 * NT);
+    const WeightBase rows{w + (size_t)n0 * W::row_bytes(K), sc + (size_t)n0 * W::row_scales(K)};
+    WeightBase base[kTiles];
+    uint32_t row[kTiles], col[NT];
+    f32x4 acc[kTiles][NT];
 #pragma unroll
-    for (int c = 0; c < NT; ++c) {
-        cols[c] = x + (size_t)min(c * 16 + lane % 16, T - 1) * K;
-        acc[0][c] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    for (int r = 0; r < kTiles; ++r) {
+        base[r] = rows;
+        row[r] = (uint32_t)min(r * 4 + lane % 16 / 4, N - 1 - n0);
+#pragma unroll
+        for (int c = 0; c < NT; ++c) acc[r][c] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
     }
-    const int steps = (K + Mxfp4Weights::STEP - 1) / Mxfp4Weights::STEP;
-    multiply_rows<Mxfp4Weights, 1, NT>(rows, cols, K, steps * wave / kWaves, steps * (wave + 1) / kWaves, acc);
 #pragma unroll
-    for (int c = 0; c < NT; ++c) s_part[wave][c][lane] = acc[0][c];
+    for (int c = 0; c < NT; ++c) col[c] = (uint32_t)min(c0 + c * 4 + lane % 16 / 4, T - 1) * (uint32_t)K * 2;
+    const int steps = (K + kStep - 1) / kStep;
+    multiply_rows<W, kTiles, NT, 4>(base, row, reinterpret_cast<const uint8_t*>(x), col, K, steps * wave / kWaves,
+                                    steps * (wave + 1) / kWaves, acc);
+#pragma unroll
+    for (int c = 0; c < NT; ++c)
+#pragma unroll
+        for (int r = 0; r < kTiles; ++r) {
+            const float v = diagonal_sum(acc[r][c]);
+            if (lane % 4 == r) s_sums[wave][c][r][lane / 16 * 4 + lane % 16 / 4] = v;
+        }
     __syncthreads();
-    for (int i = (int)threadIdx.x; i < NT * 256; i += kThreads) {
-        const int c = i / 256, l = i % 256 / 4, v = i % 4;
+    for (int o = (int)threadIdx.x; o < NT * 64; o += kThreads) {
+        const int c = o / 64, r = o / 16 % 4, at = o % 16;
         float sum = 0.0f;
 #pragma unroll
-        for (int k = 0; k < kWaves; ++k) sum += s_part[k][c][l][v];
-        const int t = c * 16 + l % 16, n = n0 + l / 16 * 4 + v;
+        for (int k = 0; k < kWaves; ++k) sum += s_sums[k][c][r][at];
+        const int t = c0 + c * 4 + at % 4, n = n0 + r * 4 + at / 4;
         if (t < T && n < N) y[(size_t)t * N + n] = (uint16_t)(pack_bf16x2(sum, 0.0f) & 0xFFFFu);
     }
 }
@@ -48,7 +62,7 @@ __global__ __launch_bounds__(kThreads) void linear_mxfp4_kernel(const uint16_t* 
 template <int NT>
 hipError_t launch_nt(const void* x, int T, int K, const uint8_t* w, const uint8_t* scales, int N, void* y,
                      hipStream_t stream) {
-    linear_mxfp4_kernel<NT><<<(N + 15) / 16, kThreads, 0, stream>>>(static_cast<const uint16_t*>(x), T, K, w, scales,
+    linear_mxfp4_kernel<NT><<<dim3((N + 15) / 16, (T + 4 * NT - 1) / (4 * NT)), kThreads, 0, stream>>>(static_cast<const uint16_t*>(x), T, K, w, scales,
                                                                     N, static_cast<uint16_t*>(y));
     return hipGetLastError();
 }
@@ -57,8 +71,8 @@ hipError_t launch_nt(const void* x, int T, int K, const uint8_t* w, const uint8_
 
 hipError_t launch_linear_mxfp4(const void* x, int T, int K, const uint8_t* w, const uint8_t* scales, int N, void* y,
                                hipStream_t stream) {
-    if (T <= 16) return launch_nt<1>(x, T, K, w, scales, N, y, stream);
-    if (T <= 32) return launch_nt<2>(x, T, K, w, scales, N, y, stream);
+    if (T <= 4) return launch_nt<1>(x, T, K, w, scales, N, y, stream);
+    if (T <= 8) return launch_nt<2>(x, T, K, w, scales, N, y, stream);
     return launch_nt<4>(x, T, K, w, scales, N, y, stream);
 }
 

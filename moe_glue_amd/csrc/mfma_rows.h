@@ -1,24 +1,27 @@
-// Products of a few tokens with streamed weight rows, shared by the few-token
-// layer (decode_layer.hip) and the MXFP4 linear (linear.hip).
+// Products of a few tokens with streamed weight rows, for the few-token layer
+// (decode_layer.hip) and the MXFP4 linear (linear.hip).
 //
-// D = A B by v_mfma_f32_16x16x32_bf16: A holds 16 weight rows, B 16 tokens
-// (columns).  Lane l has row (and column) l % 16 and the k quarter q = l / 16;
-// its 4 accumulators are rows 4q .. 4q+3 of column l % 16.  A dot product does
-// not mind the order of its terms, so a lane may take any 8 k per instruction
-// as long as A and B agree: weights are always loaded 16 bytes a lane, straight
-// from memory to registers in the layout that they have there.
+// v_mfma_f32_16x16x32_bf16 multiplies 16 rows by 16 columns over 32 k: lane l
+// holds 8 k of row (of A) and of column (of B) l % 16, which 8 of the 32 by its
+// quarter l / 16.  A weight row per lane would make neighbouring lanes load from
+// different rows, and a wave's 16-byte loads then go through the address path
+// one lane at a time (64 clocks a KiB instead of 16: measured on a 16 MB matrix
+// in cache, 5.4 us against 3.3).  So the 16 rows are 4 weight rows times 4
+// segments of k, and the 16 columns 4 tokens times the same segments:
 //
-//   bf16   a step is 32 k: lane q takes k = 32 s + 8 q .. +7, one MFMA
-//   MXFP4  a step is 128 k: 16 bytes are the 32 codes of one scale block,
-//          k = 128 s + 32 q .. +31, and four MFMAs take 8 of them each.
-//          E2M1 times 2^e has a 2-bit significand, so the widening to bf16
-//          (v_cvt_scalef32_pk_bf16_fp4, scale included) is exact.
+//   lane l: row (column) r = l % 16 / 4, segment s = l % 4, quarter q = l / 16
+//           k = 128 step + 32 q + 8 s .. + 7
 //
-// With few tokens most of a tile's columns repeat the last token; the matrix
-// cores have that to spare, the weights' stream is what bounds these kernels.
+// Four neighbouring lanes load 64 consecutive bytes and the 16 lanes of a row
+// 256.  Of the products only those of equal segments are wanted: the sum of
+// accumulator s over the four lanes of a quad is token c = l % 16 / 4 times row
+// q (diagonal_sum).  Three quarters of the multiplications are thrown away; with
+// a few tokens an expert the matrix cores have that to spare.
+//
+// MXFP4: a lane's 8 codes are one dword, and the four lanes of a quarter share
+// the scale block of 32 columns.  E2M1 times 2^e has a 2-bit significand, so
+// the widening to bf16 (v_cvt_scalef32_pk_bf16_fp4, scale included) is exact.
 #pragma once
-
-#include <type_traits>
 
 #include "device_common.h"
 
@@ -27,123 +30,111 @@ namespace moe {
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 
-// A lane's weight row: its first byte, and its scales.
-struct WeightRow {
+constexpr int kStep = 128;  // k per step of a wave: 8 for each lane of a row
+
+// A wave-uniform offset that the compiler cannot see to be one.  (Pointers stay
+// sums of a kernel argument and such an offset: then loads are global ones with
+// a scalar base.)
+__device__ __forceinline__ size_t uniform_offset(size_t v) {
+    return (size_t)uniform((uint32_t)(v >> 32)) << 32 | uniform((uint32_t)v);
+}
+__device__ __forceinline__ int wave_index() { return (int)uniform(threadIdx.x / kWave); }
+
+// Weight rows of one matrix part: row i's codes at w + i * row_bytes(K), its
+// scales at scales + i * row_scales(K); w and scales are uniform.
+struct WeightBase {
     const uint8_t* w;
     const uint8_t* scales;
 };
 
 struct Bf16Weights {
-    static constexpr int STEP = 32;   // k per step
-    static constexpr int SUB = 1;     // MFMAs per step
-    static constexpr int BATCH = 8;   // steps whose loads are issued together
-    struct Frag {
-        u32x4 v;
-    };
-    static __device__ __forceinline__ size_t row_bytes(int K) { return (size_t)K * 2; }
-    static __device__ __forceinline__ size_t row_scales(int) { return 0; }
-    static __device__ __forceinline__ Frag load(const WeightRow& r, uint32_t k) {
-        return {*reinterpret_cast<const u32x4*>(r.w + (size_t)k * 2)};
+    using Frag = u32x4;
+    static __device__ __forceinline__ uint32_t row_bytes(int K) { return (uint32_t)K * 2; }
+    static __device__ __forceinline__ uint32_t row_scales(int) { return 0; }
+    static __device__ __forceinline__ Frag load(const WeightBase& b, uint32_t row, int K, uint32_t k) {
+        return *reinterpret_cast<const u32x4*>(b.w + (row * row_bytes(K) + k * 2));
     }
-    static __device__ __forceinline__ void clear(Frag& f) { f.v = u32x4{0u, 0u, 0u, 0u}; }
-    template <int M>
-    static __device__ __forceinline__ bf16x8 sub(const Frag& f) {
-        return __builtin_bit_cast(bf16x8, f.v);
-    }
+    static __device__ __forceinline__ Frag zero() { return u32x4{0u, 0u, 0u, 0u}; }
+    static __device__ __forceinline__ bf16x8 values(const Frag& f) { return __builtin_bit_cast(bf16x8, f); }
 };
 
 struct Mxfp4Weights {
-    static constexpr int STEP = 128;
-    static constexpr int SUB = 4;
-    static constexpr int BATCH = 2;
     struct Frag {
-        u32x4 v;
+        uint32_t codes;
         uint32_t scale;  // E8M0 byte
     };
-    static __device__ __forceinline__ size_t row_bytes(int K) { return (size_t)K / 2; }
-    static __device__ __forceinline__ size_t row_scales(int K) { return (size_t)K / 32; }
-    static __device__ __forceinline__ Frag load(const WeightRow& r, uint32_t k) {
-        return {*reinterpret_cast<const u32x4*>(r.w + k / 2), (uint32_t)r.scales[k / 32]};
+    static __device__ __forceinline__ uint32_t row_bytes(int K) { return (uint32_t)K / 2; }
+    static __device__ __forceinline__ uint32_t row_scales(int K) { return (uint32_t)K / 32; }
+    static __device__ __forceinline__ Frag load(const WeightBase& b, uint32_t row, int K, uint32_t k) {
+        return {*reinterpret_cast<const uint32_t*>(b.w + (row * row_bytes(K) + k / 2)),
+                (uint32_t)b.scales[row * row_scales(K) + k / 32]};
     }
-    static __device__ __forceinline__ void clear(Frag& f) {
-        f.v = u32x4{0u, 0u, 0u, 0u};
-        f.scale = 127u;
-    }
+    static __device__ __forceinline__ Frag zero() { return {0u, 127u}; }
     // 2^(b - 127) as fp32: exponent field b; b = 0 is a subnormal, 255 is NaN
     static __device__ __forceinline__ float scale_value(uint32_t b) {
         const uint32_t u = b == 0u ? 0x00400000u : b == 255u ? 0x7FC00000u : b << 23;
         return __builtin_bit_cast(float, u);
     }
-    template <int M>
-    static __device__ __forceinline__ bf16x8 sub(const Frag& f) {
+    static __device__ __forceinline__ bf16x8 values(const Frag& f) {
         const float s = scale_value(f.scale);
-        const uint32_t c = f.v[M];
-        const bf16x2 a = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c, s, 0);
-        const bf16x2 b = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c, s, 1);
-        const bf16x2 d = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c, s, 2);
-        const bf16x2 e = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c, s, 3);
-        return bf16x8{a[0], a[1], b[0], b[1], d[0], d[1], e[0], e[1]};
+        const bf16x2 a = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(f.codes, s, 0);
+        const bf16x2 b = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(f.codes, s, 1);
+        const bf16x2 c = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(f.codes, s, 2);
+        const bf16x2 d = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(f.codes, s, 3);
+        return bf16x8{a[0], a[1], b[0], b[1], c[0], c[1], d[0], d[1]};
     }
 };
 
-// acc[r][c] += rows r (16 each) times columns c (16 each) over the steps
-// [s0, s1) of K.  col[c]: the lane's column, its first bf16.  Steps past the
-// range repeat the last one's loads (the addresses stay inside the row) and
-// are not multiplied; in a step that K ends inside, lanes past K hold zeros.
-template <class W, int RT, int NT>
-__device__ __forceinline__ void multiply_rows(const WeightRow (&row)[RT], const uint16_t* const (&col)[NT], int K,
-                                              int s0, int s1, f32x4 (&acc)[RT][NT]) {
-    constexpr int PIECE = W::STEP / 4;  // k of a lane in a step
-    const uint32_t q = (threadIdx.x % kWave) / 16;
-    const uint32_t last = (uint32_t)K - PIECE;
-    for (int s = s0; s < s1; s += W::BATCH) {
-        typename W::Frag a[W::BATCH][RT];
-        u32x4 b[W::BATCH][NT][W::SUB];
+// acc[r][c] += the lane's row of base[r] (row[r], counted from base[r]) times
+// its column c (first bf16 at x + col[c], in bytes) over the steps [s0, s1) of
+// K.  U steps' loads are issued together; steps past the range repeat the last
+// one's loads (addresses stay inside the row) and are not multiplied.  In a
+// step that K ends inside, lanes past K hold zeros.
+template <class W, int RT, int NT, int U>
+__device__ __forceinline__ void multiply_rows(const WeightBase (&base)[RT], const uint32_t (&row)[RT],
+                                              const uint8_t* x, const uint32_t (&col)[NT], int K, int s0, int s1,
+                                              f32x4 (&acc)[RT][NT]) {
+    const uint32_t lane = threadIdx.x % kWave;
+    const uint32_t piece = lane / 16 * 32 + lane % 4 * 8;
+    const uint32_t last = (uint32_t)K - 8;
+    for (int s = s0; s < s1; s += U) {
+        typename W::Frag a[U][RT];
+        u32x4 b[U][NT];
 #pragma unroll
-        for (int u = 0; u < W::BATCH; ++u) {
-            const uint32_t k = min((uint32_t)min(s + u, s1 - 1) * W::STEP + q * PIECE, last);
+        for (int u = 0; u < U; ++u) {
+            const uint32_t k = min((uint32_t)min(s + u, s1 - 1) * kStep + piece, last);
 #pragma unroll
-            for (int r = 0; r < RT; ++r) a[u][r] = W::load(row[r], k);
+            for (int r = 0; r < RT; ++r) a[u][r] = W::load(base[r], row[r], K, k);
+#pragma unroll
+            for (int c = 0; c < NT; ++c) b[u][c] = *reinterpret_cast<const u32x4*>(x + (col[c] + k * 2));
         }
 #pragma unroll
-        for (int u = 0; u < W::BATCH; ++u) {
-            const uint32_t k = min((uint32_t)min(s + u, s1 - 1) * W::STEP + q * PIECE, last);
-#pragma unroll
-            for (int c = 0; c < NT; ++c)
-#pragma unroll
-                for (int m = 0; m < W::SUB; ++m)
-                    b[u][c][m] = *reinterpret_cast<const u32x4*>(col[c] + k + m * 8);
-        }
-#pragma unroll
-        for (int u = 0; u < W::BATCH; ++u) {
+        for (int u = 0; u < U; ++u) {
             if (s + u >= s1) continue;  // uniform
-            if ((s + u + 1) * W::STEP > K && (uint32_t)(s + u) * W::STEP + q * PIECE > last) {
+            if ((s + u + 1) * kStep > K && (uint32_t)(s + u) * kStep + piece > last) {
 #pragma unroll
-                for (int r = 0; r < RT; ++r) W::clear(a[u][r]);
+                for (int r = 0; r < RT; ++r) a[u][r] = W::zero();
+#pragma unroll
+                for (int c = 0; c < NT; ++c) b[u][c] = u32x4{0u, 0u, 0u, 0u};
+            }
+#pragma unroll
+            for (int r = 0; r < RT; ++r) {
+                const bf16x8 av = W::values(a[u][r]);
 #pragma unroll
                 for (int c = 0; c < NT; ++c)
-#pragma unroll
-                    for (int m = 0; m < W::SUB; ++m) b[u][c][m] = u32x4{0u, 0u, 0u, 0u};
-            }
-            const auto mul = [&](auto sub_index) {
-                constexpr int M = decltype(sub_index)::value;
-#pragma unroll
-                for (int r = 0; r < RT; ++r) {
-                    const bf16x8 av = W::template sub<M>(a[u][r]);
-#pragma unroll
-                    for (int c = 0; c < NT; ++c)
-                        acc[r][c] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
-                            av, __builtin_bit_cast(bf16x8, b[u][c][M]), acc[r][c], 0, 0, 0);
-                }
-            };
-            mul(std::integral_constant<int, 0>{});
-            if constexpr (W::SUB == 4) {
-                mul(std::integral_constant<int, 1>{});
-                mul(std::integral_constant<int, 2>{});
-                mul(std::integral_constant<int, 3>{});
+                    acc[r][c] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(av, __builtin_bit_cast(bf16x8, b[u][c]),
+                                                                        acc[r][c], 0, 0, 0);
             }
         }
     }
+}
+
+// The product of row l / 16 with column l % 16 / 4, in all four lanes of the
+// quad: segment s of both is accumulator s of the quad's lane s.
+__device__ __forceinline__ float diagonal_sum(const f32x4& a) {
+    const uint32_t s = threadIdx.x % 4;
+    const float v = s < 2 ? (s == 0 ? a[0] : a[1]) : (s == 2 ? a[2] : a[3]);
+    return __builtin_bit_cast(float, group_reduce<4, Op::FAdd>(__builtin_bit_cast(uint32_t, v)));
 }
 
 }  // namespace moe
