@@ -20,7 +20,7 @@
 //
 // Launch 2.  A workgroup owns a few output columns (4 rows of w_down, 8 with
 // MXFP4) for every token, so the sum over experts needs no atomics and no third
-// launch.  Its waves deal the active experts, and split K when there are few.
+// launch.  Its waves deal the entries, and split K when there are few.
 // fp32 y meets in LDS and is summed over j in order, so the same call always
 // gives the same bits.
 #include "kernels.h"
@@ -38,12 +38,21 @@ constexpr int kMaxTokens = kDecodeLayerMaxTokens;
 static_assert(kMaxTokens <= 64, "one bitmap word per expert");
 constexpr int kMaxSlots = kMaxTokens * kKMax;
 
+// The work is dealt in entries: an active expert with up to kEntryTokens of its
+// tokens (an expert with more has several, next to each other), so that entries
+// cost about the same however the router's choices are spread.
+template <class W>
+constexpr int kEntryTokens = 16;
+template <>
+constexpr int kEntryTokens<Mxfp4Weights> = 8;  // by registers, see mfma_rows.h
+constexpr int kMaxEntries = kEMax + kMaxSlots / 8;
+
 // Front of the workspace, written by launch 1 for launch 2.
 struct Tables {
-    int32_t n;                  // active experts
-    int32_t expert[kEMax];      // in ascending order
-    int32_t first[kEMax + 1];   // first p of each; first[n] = number of pairs
-    int32_t dest[kMaxSlots];    // p of slot t*k + j
+    int32_t n;                       // entries
+    int32_t expert[kMaxEntries];     // in ascending order
+    int32_t first[kMaxEntries + 1];  // first p of each; first[n] = number of pairs
+    int32_t dest[kMaxSlots];         // p of slot t*k + j
 };
 static_assert(sizeof(Tables) <= kDecodeLayerTableBytes, "tables outgrow their part of the workspace");
 
@@ -53,62 +62,96 @@ __device__ __forceinline__ float silu_mul(float g, float u) {
     return g * __builtin_amdgcn_rcpf(1.0f + e) * u;
 }
 
-// Row tiles of an item: 16 gate rows, then their 16 up rows, 4 to a tile.
-constexpr int kItemTiles = 8;
+// Row quads (4 gate rows and their 4 up rows) that a wave multiplies together
+// where it has K to itself: with MXFP4 a column's loads cost as much as four
+// row tiles', so two quads share them.
+template <class W>
+constexpr int kWaveQuads = 1;
+template <>
+constexpr int kWaveQuads<Mxfp4Weights> = 2;
+// Steps of loads in flight for a task of RT row and NT column tiles.
+template <class W, int RT, int NT>
+constexpr int kInFlight = NT == 1 ? 6 : NT == 2 ? 4 : 2;
+template <int RT, int NT>
+constexpr int kInFlight<Mxfp4Weights, RT, NT> = NT == 1 ? 4 : 2;
 
-// One wave's sums of an item: [row tile][row of the tile * 4 + column].
-template <int NT>
-using ItemSums = float[NT][kItemTiles][16];
+// Where a task's rows and tokens are: row quad `quad` (4 gate rows and their 4
+// up rows) of expert e; of its tokens, the set bits of mask, m from number c0
+// on; and their rows p0, p0 + 1, .. of act.
+struct GateUpTask {
+    uint32_t e, quad, p0;
+    int c0, m;
+    unsigned long long mask;
+};
 
-// Columns c0 .. c0 + 4 NT - 1 of an item.  `flip` alternates between the two
-// halves of `sums`, so one barrier an item is enough: a wave that writes the
-// half used two items ago has passed the barrier after it was read.
-template <class W, int NT>
-__device__ __forceinline__ void gate_up_item(const uint8_t* x, int H, const uint8_t* w, const uint8_t* sc, int I,
-                                             uint32_t e, uint32_t i0, unsigned long long mask, int m, int c0,
-                                             uint32_t p0, uint16_t* __restrict__ act, ItemSums<NT>* sums) {
+// g, u: the products of QT row quads with the task's tokens over the steps
+// [s0, s1), row l / 16 and column l % 16 / 4 of each tile in lane l.
+template <class W, int QT, int NT>
+__device__ __forceinline__ void gate_up_product(const GateUpTask& t, const uint8_t* x, int H, const uint8_t* w,
+                                                const uint8_t* sc, int I, int s0, int s1, float (&g)[QT][NT],
+                                                float (&u)[QT][NT]) {
     const int lane = (int)(threadIdx.x % kWave);
-    const int wave = wave_index();
-    const size_t first = (size_t)e * 2 * I + i0;
+    const size_t first = (size_t)t.e * 2 * I + t.quad * 4;
     const WeightBase gate{w + uniform_offset(first * W::row_bytes(H)), sc + uniform_offset(first * W::row_scales(H))};
     const WeightBase up{gate.w + (size_t)I * W::row_bytes(H), gate.scales + (size_t)I * W::row_scales(H)};
-    WeightBase base[kItemTiles];
-    uint32_t row[kItemTiles], col[NT];
+    WeightBase base[2 * QT];
+    uint32_t row[2 * QT], col[NT];
+    f32x4 acc[2 * QT][NT];
 #pragma unroll
-    for (int r = 0; r < kItemTiles; ++r) {
-        base[r] = r < kItemTiles / 2 ? gate : up;
-        row[r] = min((uint32_t)(r % (kItemTiles / 2) * 4 + lane % 16 / 4), (uint32_t)I - 1 - i0);
+    for (int r = 0; r < 2 * QT; ++r) {
+        base[r] = r % 2 == 0 ? gate : up;
+        row[r] = (uint32_t)(r / 2 * 4 + lane % 16 / 4);
+#pragma unroll
+        for (int c = 0; c < NT; ++c) acc[r][c] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
     }
 #pragma unroll
     for (int c = 0; c < NT; ++c)
-        col[c] = (uint32_t)select_bit(mask, min(c0 + c * 4 + lane % 16 / 4, m - 1)) * (uint32_t)H * 2;
-    f32x4 acc[kItemTiles][NT];
+        col[c] = (uint32_t)select_bit(t.mask, t.c0 + min(c * 4 + lane % 16 / 4, t.m - 1)) * (uint32_t)H * 2;
+    multiply_rows<W, 2 * QT, NT, kInFlight<W, 2 * QT, NT>>(base, row, x, col, H, s0, s1, acc);
 #pragma unroll
-    for (int r = 0; r < kItemTiles; ++r)
+    for (int q = 0; q < QT; ++q)
 #pragma unroll
-        for (int c = 0; c < NT; ++c) acc[r][c] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-    const int steps = (H + kStep - 1) / kStep;
-    multiply_rows<W, kItemTiles, NT, (NT == 1 ? 2 : 1)>(base, row, x, col, H, steps * wave / kWaves, steps * (wave + 1) / kWaves, acc);
-#pragma unroll
-    for (int c = 0; c < NT; ++c)
-#pragma unroll
-        for (int r = 0; r < kItemTiles; ++r) {
-            const float v = diagonal_sum(acc[r][c]);
-            if (lane % 4 == r % 4) sums[wave][c][r][lane / 16 * 4 + lane % 16 / 4] = v;
+        for (int c = 0; c < NT; ++c) {
+            g[q][c] = diagonal_sum(acc[2 * q][c]);
+            u[q][c] = diagonal_sum(acc[2 * q + 1][c]);
         }
-    __syncthreads();
-    for (int o = (int)threadIdx.x; o < NT * 64; o += kThreads) {
-        const int c = o / 64, r = o / 16 % 4, at = o % 16;
-        float g = 0.0f, u = 0.0f;
+}
+
+__device__ __forceinline__ uint16_t swiglu_bf16(float g, float u) {
+    return (uint16_t)(pack_bf16x2(silu_mul(g, u), 0.0f) & 0xFFFFu);
+}
+
+// All of K by one wave: the outputs go straight to act.
+template <class W, int QT, int NT>
+__device__ __forceinline__ void gate_up_whole(const GateUpTask& t, const uint8_t* x, int H, const uint8_t* w,
+                                              const uint8_t* sc, int I, uint16_t* __restrict__ act) {
+    float g[QT][NT], u[QT][NT];
+    gate_up_product<W, QT, NT>(t, x, H, w, sc, I, 0, steps_of<W>(H), g, u);
+    const int lane = (int)(threadIdx.x % kWave);
 #pragma unroll
-        for (int k = 0; k < kWaves; ++k) {
-            g += sums[k][c][r][at];
-            u += sums[k][c][r + kItemTiles / 2][at];
+    for (int q = 0; q < QT; ++q)
+#pragma unroll
+        for (int c = 0; c < NT; ++c) {
+            const int column = c * 4 + lane % 16 / 4;
+            if (lane % 4 == (q * NT + c) % 4 && column < t.m)
+                act[(size_t)(t.p0 + column) * I + (t.quad + q) * 4 + lane / 16] = swiglu_bf16(g[q][c], u[q][c]);
         }
-        const int column = c0 + c * 4 + at % 4;
-        const uint32_t i = i0 + r * 4 + at / 4;
-        if (column < m && i < (uint32_t)I)
-            act[(size_t)(p0 + column) * I + i] = (uint16_t)(pack_bf16x2(silu_mul(g, u), 0.0f) & 0xFFFFu);
+}
+
+// A part of K: the partial sums go to LDS, [column tile][gate, up][16].
+constexpr int kPartSums = 4 * 2 * 16;
+
+template <class W, int NT>
+__device__ __forceinline__ void gate_up_part(const GateUpTask& t, const uint8_t* x, int H, const uint8_t* w,
+                                             const uint8_t* sc, int I, int s0, int s1, float* sums) {
+    float g[1][NT], u[1][NT];
+    gate_up_product<W, 1, NT>(t, x, H, w, sc, I, s0, s1, g, u);
+    const int lane = (int)(threadIdx.x % kWave);
+    const int at = lane / 16 * 4 + lane % 16 / 4;
+#pragma unroll
+    for (int c = 0; c < NT; ++c) {
+        if (lane % 4 == 0) sums[c * 32 + at] = g[0][c];
+        if (lane % 4 == 1) sums[c * 32 + 16 + at] = u[0][c];
     }
 }
 
@@ -121,11 +164,11 @@ __global__ __launch_bounds__(kThreads, 4) void decode_gate_up_kernel(
     constexpr int TOK_PER_PASS = kThreads / G;
     __shared__ int32_t s_ids[kMaxSlots];
     __shared__ unsigned long long s_mask[kEMax];  // bit t: token t picked the expert
-    __shared__ int32_t s_expert[kEMax];
-    __shared__ int32_t s_first[kEMax + 1];
+    __shared__ int32_t s_entry[kMaxEntries];  // expert, and number of the entry among its own from bit 16 on
+    __shared__ int32_t s_first[kMaxEntries + 1];
     __shared__ int32_t s_off[kEMax];  // first p by expert
     __shared__ int32_t s_n;
-    __shared__ float s_sums[2][kWaves * 2 * kItemTiles * 16];  // two halves for up to 2 column tiles
+    __shared__ float s_sums[kWaves][kPartSums];
 
     const int lane = (int)(threadIdx.x % kWave);
     const int wave = wave_index();
@@ -141,21 +184,23 @@ __global__ __launch_bounds__(kThreads, 4) void decode_gate_up_kernel(
             for (int r = gl; r < k; r += G) atomicOr(&s_mask[s_ids[t * k + r]], 1ull << t);
     }
     __syncthreads();
-    if (wave == 0) {  // the active experts, and the first p of each
+    constexpr int TOKENS = kEntryTokens<W>;
+    if (wave == 0) {  // the entries, and the first p of each
         int n = 0, run = 0;
         for (int e0 = 0; e0 < E; e0 += kWave) {
             const int e = e0 + lane;
             const int cnt = e < E ? __popcll(s_mask[e]) : 0;
-            const unsigned long long some = __ballot(cnt > 0);
-            const int incl = wave_inclusive_sum(cnt);
-            const int at = n + __popcll(some & ((1ull << lane) - 1ull));
-            if (cnt > 0) {
-                s_expert[at] = e;
-                s_first[at] = run + incl - cnt;
-                s_off[e] = run + incl - cnt;
+            const int own = (cnt + TOKENS - 1) / TOKENS;
+            const int incl = wave_inclusive_sum(cnt | own << 16);  // both counts stay below 2^16
+            const int p0 = run + (incl & 0xFFFF) - cnt, at = n + (incl >> 16) - own;
+            if (cnt > 0) s_off[e] = p0;
+            for (int i = 0; i < own; ++i) {
+                s_entry[at + i] = e | i << 16;
+                s_first[at + i] = p0 + i * TOKENS;
             }
-            n += __popcll(some);
-            run += __builtin_amdgcn_readlane(incl, kWave - 1);
+            const int total = __builtin_amdgcn_readlane(incl, kWave - 1);
+            n += total >> 16;
+            run += total & 0xFFFF;
         }
         if (lane == 0) {
             s_n = n;
@@ -167,7 +212,7 @@ __global__ __launch_bounds__(kThreads, 4) void decode_gate_up_kernel(
     if (writer) {
         if (threadIdx.x == 0) tables->n = n;
         for (int a = (int)threadIdx.x; a <= n; a += kThreads) {
-            if (a < n) tables->expert[a] = s_expert[a];
+            if (a < n) tables->expert[a] = s_entry[a] & 0xFFFF;
             tables->first[a] = s_first[a];
         }
         for (int s = (int)threadIdx.x; s < T * k; s += kThreads) {
@@ -175,25 +220,72 @@ __global__ __launch_bounds__(kThreads, 4) void decode_gate_up_kernel(
             tables->dest[s] = s_off[e] + __popcll(s_mask[e] & ((1ull << (s / k)) - 1ull));
         }
     }
-    const int tiles = (I + 15) / 16;
-    int half = 0;
-    for (int it = (int)blockIdx.x; it < n * tiles; it += (int)gridDim.x) {
-        const int a = it / tiles;
-        const uint32_t e = uniform((uint32_t)s_expert[a]);
-        const unsigned long long mask = s_mask[e];
-        const int m = (int)uniform((uint32_t)__popcll(mask));
-        const uint32_t i0 = (uint32_t)(it - a * tiles) * 16;
-        const uint32_t p0 = uniform((uint32_t)s_first[a]);
-        const uint8_t* xb = reinterpret_cast<const uint8_t*>(x);
-        for (int c0 = 0; c0 < m; c0 += 8) {
-            if (m - c0 <= 4)
-                gate_up_item<W, 1>(xb, H, w, sc, I, e, i0, mask, m, c0, p0, act,
-                                   reinterpret_cast<ItemSums<1>*>(s_sums[half]));
-            else
-                gate_up_item<W, 2>(xb, H, w, sc, I, e, i0, mask, m, c0, p0, act,
-                                   reinterpret_cast<ItemSums<2>*>(s_sums[half]));
-            half ^= 1;
+    const uint32_t per = (uint32_t)I / 4;  // row quads of an expert
+    const uint32_t all = uniform((uint32_t)n) * per;
+    const uint8_t* xb = reinterpret_cast<const uint8_t*>(x);
+    const auto task_of = [&](uint32_t at) {
+        GateUpTask t;
+        const uint32_t a = at / per;
+        const uint32_t entry = uniform((uint32_t)s_entry[a]);
+        t.quad = at - a * per;
+        t.e = entry & 0xFFFFu;
+        t.c0 = (int)(entry >> 16) * TOKENS;
+        t.p0 = uniform((uint32_t)s_first[a]);
+        t.m = (int)uniform((uint32_t)s_first[a + 1]) - (int)t.p0;
+        t.mask = s_mask[t.e];
+        return t;
+    };
+    // whole rounds of the grid, QT quads a wave (I / 4 is a multiple of QT: a
+    // wave's quads are one expert's).  Neighbouring workgroups take neighbouring
+    // rows, so that the rows of an expert with many tokens, which take longer,
+    // are spread over all of them.
+    constexpr uint32_t QT = kWaveQuads<W>;
+    const uint32_t round = gridDim.x * kWaves * QT;
+    const uint32_t whole = all / round * round;
+    for (uint32_t at = (blockIdx.x * kWaves + (uint32_t)wave) * QT; at < whole; at += round) {
+        const GateUpTask t = task_of(at);
+        if (t.m <= 4)
+            gate_up_whole<W, QT, 1>(t, xb, H, w, sc, I, act);
+        else if (t.m <= 8 || TOKENS == 8)
+            gate_up_whole<W, QT, 2>(t, xb, H, w, sc, I, act);
+        else if constexpr (TOKENS == 16)
+            gate_up_whole<W, QT, 4>(t, xb, H, w, sc, I, act);
+    }
+    // this workgroup's share of the quads that are left, eight or fewer at a
+    // time: `parts` waves split the K of each, and meet in LDS
+    const int steps = steps_of<W>(H);
+    const uint32_t begin = whole + (uint32_t)((uint64_t)(all - whole) * blockIdx.x / gridDim.x);
+    const uint32_t left = whole + (uint32_t)((uint64_t)(all - whole) * (blockIdx.x + 1) / gridDim.x) - begin;
+    for (uint32_t done = 0; done < left; done += kWaves) {
+        const uint32_t now = min(left - done, (uint32_t)kWaves);
+        int parts = kWaves;
+        while (parts * now > kWaves) parts /= 2;
+        const uint32_t mine = done + (uint32_t)(wave / parts);
+        const int part = wave % parts;
+        const bool busy = mine < done + now;  // uniform
+        GateUpTask t{};
+        if (busy) {
+            t = task_of(begin + mine);
+            const int s0 = steps * part / parts, s1 = steps * (part + 1) / parts;
+            if (t.m <= 4)
+                gate_up_part<W, 1>(t, xb, H, w, sc, I, s0, s1, s_sums[wave]);
+            else if (t.m <= 8 || TOKENS == 8)
+                gate_up_part<W, 2>(t, xb, H, w, sc, I, s0, s1, s_sums[wave]);
+            else if constexpr (TOKENS == 16)
+                gate_up_part<W, 4>(t, xb, H, w, sc, I, s0, s1, s_sums[wave]);
         }
+        __syncthreads();
+        const int column = lane / 16 * 4 + lane % 4;
+        if (busy && part == 0 && column < t.m) {
+            const int at = lane / 16 * 32 + lane % 16;
+            float g = 0.0f, u = 0.0f;
+            for (int k = 0; k < parts; ++k) {
+                g += s_sums[wave + k][at];
+                u += s_sums[wave + k][at + 16];
+            }
+            act[(size_t)(t.p0 + column) * I + t.quad * 4 + lane % 16 / 4] = swiglu_bf16(g, u);
+        }
+        __syncthreads();
     }
 }
 
@@ -203,9 +295,14 @@ constexpr int kDownTiles = 1;
 template <>
 constexpr int kDownTiles<Mxfp4Weights> = 2;
 
+template <class W, int NT>
+constexpr int kDownInFlight = NT == 1 ? 8 : NT == 2 ? 4 : 2;
+template <int NT>
+constexpr int kDownInFlight<Mxfp4Weights, NT> = NT == 1 ? 4 : 2;
+
 constexpr int kMaxY = kMaxSlots;  // y entries of a workgroup: pairs times K parts
 
-// K parts of an expert's rows: enough that the eight waves have two tasks each,
+// K parts of an entry's rows: enough that the eight waves have two tasks each,
 // as long as y holds them.  One part always fits: there are at most kMaxSlots
 // pairs.
 __device__ __forceinline__ int k_parts(int n, int pairs) {
@@ -231,7 +328,7 @@ __device__ __forceinline__ void down_columns(const WeightBase& rows, int left, c
     }
 #pragma unroll
     for (int c = 0; c < NT; ++c) col[c] = (uint32_t)min(p0 + c * 4 + lane % 16 / 4, end - 1) * (uint32_t)I * 2;
-    multiply_rows<W, RT, NT, 4>(base, row, act, col, I, s0, s1, acc);
+    multiply_rows<W, RT, NT, kDownInFlight<W, NT>>(base, row, act, col, I, s0, s1, acc);
 #pragma unroll
     for (int c = 0; c < NT; ++c) {
         const int p = p0 + c * 4 + lane % 16 / 4;
@@ -263,7 +360,7 @@ __global__ __launch_bounds__(kThreads) void decode_down_kernel(int T, int k, con
         s_dest[s] = tables->dest[s];
     }
     const int parts = k_parts(n, pairs);
-    const int steps = (I + kStep - 1) / kStep;
+    const int steps = steps_of<W>(I);
     const uint8_t* actb = reinterpret_cast<const uint8_t*>(act);
     for (int task = wave; task < n * parts; task += kWaves) {
         const int a = task / parts, part = task - a * parts;
@@ -272,12 +369,12 @@ __global__ __launch_bounds__(kThreads) void decode_down_kernel(int T, int k, con
         const int begin = tables->first[a], end = tables->first[a + 1];
         const int s0 = steps * part / parts, s1 = steps * (part + 1) / parts;
         float* y = s_y + part * pairs * ROWS;
-        for (int p0 = begin; p0 < end; p0 += 8) {
-            if (end - p0 <= 4)
-                down_columns<W, 1>(rows, H - h0, actb, I, p0, end, s0, s1, y);
-            else
-                down_columns<W, 2>(rows, H - h0, actb, I, p0, end, s0, s1, y);
-        }
+        if (end - begin <= 4)
+            down_columns<W, 1>(rows, H - h0, actb, I, begin, end, s0, s1, y);
+        else if (end - begin <= 8 || kEntryTokens<W> == 8)
+            down_columns<W, 2>(rows, H - h0, actb, I, begin, end, s0, s1, y);
+        else if constexpr (kEntryTokens<W> == 16)
+            down_columns<W, 4>(rows, H - h0, actb, I, begin, end, s0, s1, y);
     }
     __syncthreads();
     for (int i = (int)threadIdx.x; i < T * ROWS; i += kThreads) {
@@ -300,8 +397,8 @@ hipError_t launch_gv(const DecodeLayerArgs& a, hipStream_t stream) {
     Tables* tables = static_cast<Tables*>(a.workspace);
     uint16_t* act = reinterpret_cast<uint16_t*>(static_cast<char*>(a.workspace) + kDecodeLayerTableBytes);
     const uint16_t* x = static_cast<const uint16_t*>(a.x);
-    const int64_t most = (int64_t)(a.E < a.T * a.k ? a.E : a.T * a.k) * ((a.I + 15) / 16);
-    const int grid = (int)(most < kMaxGrid ? most : kMaxGrid);
+    const int64_t quads = (int64_t)(a.E < a.T * a.k ? a.E : a.T * a.k) * (a.I / 4);  // at most
+    const int grid = (int)(quads < kMaxGrid ? quads : kMaxGrid);
     decode_gate_up_kernel<W, G, V><<<grid, kThreads, 0, stream>>>(
         a.logits, a.bias, a.T, a.E, a.k, x, a.H, static_cast<const uint8_t*>(a.w_gate_up), a.s_gate_up, a.I,
         a.topk_ids, a.topk_weights, tables, act);

@@ -224,7 +224,7 @@ hipError_t launch_rmsnorm(const NormArgs& a, hipStream_t stream);
 constexpr int kDecodeLayerMaxTokens = MOE_DECODE_T_MAX;
 // Front part of the few-token layer's workspace: the routing tables its first
 // launch writes for its second; the activations [T*k, I] bf16 follow.
-constexpr size_t kDecodeLayerTableBytes = 8448;
+constexpr size_t kDecodeLayerTableBytes = 9472;
 inline size_t decode_layer_workspace_bytes(int T, int k, int I) {
     return kDecodeLayerTableBytes + (size_t)T * k * I * 2;
 }

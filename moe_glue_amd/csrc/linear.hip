@@ -38,8 +38,8 @@ __global__ __launch_bounds__(kThreads) void linear_mxfp4_kernel(const uint16_t* 
     }
 #pragma unroll
     for (int c = 0; c < NT; ++c) col[c] = (uint32_t)min(c0 + c * 4 + lane % 16 / 4, T - 1) * (uint32_t)K * 2;
-    const int steps = (K + kStep - 1) / kStep;
-    multiply_rows<W, kTiles, NT, 4>(base, row, reinterpret_cast<const uint8_t*>(x), col, K, steps * wave / kWaves,
+    const int steps = steps_of<W>(K);
+    multiply_rows<W, kTiles, NT, (NT == 4 ? 2 : 4)>(base, row, reinterpret_cast<const uint8_t*>(x), col, K, steps * wave / kWaves,
                                     steps * (wave + 1) / kWaves, acc);
 #pragma unroll
     for (int c = 0; c < NT; ++c)

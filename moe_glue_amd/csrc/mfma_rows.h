@@ -3,25 +3,30 @@
 //
 // v_mfma_f32_16x16x32_bf16 multiplies 16 rows by 16 columns over 32 k: lane l
 // holds 8 k of row (of A) and of column (of B) l % 16, which 8 of the 32 by its
-// quarter l / 16.  A weight row per lane would make neighbouring lanes load from
-// different rows, and a wave's 16-byte loads then go through the address path
-// one lane at a time (64 clocks a KiB instead of 16: measured on a 16 MB matrix
-// in cache, 5.4 us against 3.3).  So the 16 rows are 4 weight rows times 4
-// segments of k, and the 16 columns 4 tokens times the same segments:
+// quarter l / 16.  A vector load takes a CU 16 clocks when each four
+// neighbouring lanes stay inside one 128-byte line, whatever their width, but 64
+// when they all differ (measured, from cache) -- and a weight row per lane makes
+// them differ.  So the 16 rows are 4 weight rows times 4 segments of k, and the
+// 16 columns 4 tokens times the same segments:
 //
 //   lane l: row (column) r = l % 16 / 4, segment s = l % 4, quarter q = l / 16
-//           k = 128 step + 32 q + 8 s .. + 7
+//           k = step + (4 q + s) * P .. + P - 1
 //
-// Four neighbouring lanes load 64 consecutive bytes and the 16 lanes of a row
-// 256.  Of the products only those of equal segments are wanted: the sum of
-// accumulator s over the four lanes of a quad is token c = l % 16 / 4 times row
-// q (diagonal_sum).  Three quarters of the multiplications are thrown away; with
-// a few tokens an expert the matrix cores have that to spare.
+// Of the products only those of equal segments are wanted: the sum of
+// accumulator s over the four lanes s of a quad is token c = l % 16 / 4 times
+// row q (diagonal_sum).  Three quarters of the multiplications are thrown away;
+// with a few tokens an expert the matrix cores have that to spare.
 //
-// MXFP4: a lane's 8 codes are one dword, and the four lanes of a quarter share
-// the scale block of 32 columns.  E2M1 times 2^e has a 2-bit significand, so
-// the widening to bf16 (v_cvt_scalef32_pk_bf16_fp4, scale included) is exact.
+//   bf16   P = 8: a step is 128 k, one MFMA, 256 bytes of each row
+//   MXFP4  P = 16: a step is 256 k, two MFMAs, 128 bytes of each row (with 8
+//          bytes a lane; 4 cost as many clocks, and with 16 the neighbouring
+//          lanes' columns would lie 64 bytes apart).  Two lanes share a scale
+//          block of 32 columns.  E2M1 times 2^e has a 2-bit significand, so the
+//          widening to bf16 (v_cvt_scalef32_pk_bf16_fp4, scale included) is
+//          exact.
 #pragma once
+
+#include <type_traits>
 
 #include "device_common.h"
 
@@ -29,8 +34,6 @@ namespace moe {
 
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
-
-constexpr int kStep = 128;  // k per step of a wave: 8 for each lane of a row
 
 // A wave-uniform offset that the compiler cannot see to be one.  (Pointers stay
 // sums of a kernel argument and such an offset: then loads are global ones with
@@ -47,86 +50,160 @@ struct WeightBase {
     const uint8_t* scales;
 };
 
+// A lane's part of one row over U steps: load() fills step u's registers (and
+// scales() those of SCALE_STEPS steps), values<u, m>() gives the 8 weights of
+// its MFMA m.
 struct Bf16Weights {
-    using Frag = u32x4;
+    static constexpr int STEP = 128;
+    static constexpr int SUB = 1;          // MFMAs per step
+    static constexpr int SCALE_STEPS = 1;  // steps to a scale load (1: no scales)
+    template <int U>
+    struct Rows {
+        u32x4 v[U];
+    };
     static __device__ __forceinline__ uint32_t row_bytes(int K) { return (uint32_t)K * 2; }
     static __device__ __forceinline__ uint32_t row_scales(int) { return 0; }
-    static __device__ __forceinline__ Frag load(const WeightBase& b, uint32_t row, int K, uint32_t k) {
-        return *reinterpret_cast<const u32x4*>(b.w + (row * row_bytes(K) + k * 2));
+    template <int U>
+    static __device__ __forceinline__ void scales(Rows<U>&, int, const WeightBase&, uint32_t, int, int) {}
+    template <int U>
+    static __device__ __forceinline__ void load(Rows<U>& f, int u, const WeightBase& b, uint32_t row, int K,
+                                                uint32_t k) {
+        f.v[u] = *reinterpret_cast<const u32x4*>(b.w + (row * row_bytes(K) + k * 2));
     }
-    static __device__ __forceinline__ Frag zero() { return u32x4{0u, 0u, 0u, 0u}; }
-    static __device__ __forceinline__ bf16x8 values(const Frag& f) { return __builtin_bit_cast(bf16x8, f); }
+    template <int U>
+    static __device__ __forceinline__ void clear(Rows<U>& f, int u) {
+        f.v[u] = u32x4{0u, 0u, 0u, 0u};
+    }
+    template <int u, int M, int U>
+    static __device__ __forceinline__ bf16x8 values(const Rows<U>& f) {
+        return __builtin_bit_cast(bf16x8, f.v[u]);
+    }
 };
 
 struct Mxfp4Weights {
-    struct Frag {
-        uint32_t codes;
-        uint32_t scale;  // E8M0 byte
+    static constexpr int STEP = 256;
+    static constexpr int SUB = 2;
+    static constexpr int SCALE_STEPS = 2;
+    template <int U>
+    struct Rows {
+        u32x2 codes[U];
+        uint32_t scale[(U + 1) / 2];  // even lanes: step 2 g's, odd lanes: step 2 g + 1's, as fp32 bits
     };
     static __device__ __forceinline__ uint32_t row_bytes(int K) { return (uint32_t)K / 2; }
     static __device__ __forceinline__ uint32_t row_scales(int K) { return (uint32_t)K / 32; }
-    static __device__ __forceinline__ Frag load(const WeightBase& b, uint32_t row, int K, uint32_t k) {
-        return {*reinterpret_cast<const uint32_t*>(b.w + (row * row_bytes(K) + k / 2)),
-                (uint32_t)b.scales[row * row_scales(K) + k / 32]};
+    // One byte load for two steps: of the two lanes that share a block in both,
+    // each fetches one step's byte, and values() hands it over.  2^(b - 127) has
+    // exponent field b; b = 0 is a subnormal, 255 is NaN.
+    template <int U>
+    static __device__ __forceinline__ void scales(Rows<U>& f, int g, const WeightBase& b, uint32_t row, int K,
+                                                  int step) {
+        const uint32_t lane = threadIdx.x % kWave;
+        const uint32_t at = min((uint32_t)(step + lane % 2) * (STEP / 32) + lane / 16 * 2 + lane % 4 / 2,
+                                row_scales(K) - 1);
+        const uint32_t v = b.scales[row * row_scales(K) + at];
+        f.scale[g] = v == 0u ? 0x00400000u : v == 255u ? 0x7FC00000u : v << 23;
     }
-    static __device__ __forceinline__ Frag zero() { return {0u, 127u}; }
-    // 2^(b - 127) as fp32: exponent field b; b = 0 is a subnormal, 255 is NaN
-    static __device__ __forceinline__ float scale_value(uint32_t b) {
-        const uint32_t u = b == 0u ? 0x00400000u : b == 255u ? 0x7FC00000u : b << 23;
-        return __builtin_bit_cast(float, u);
+    template <int U>
+    static __device__ __forceinline__ void load(Rows<U>& f, int u, const WeightBase& b, uint32_t row, int K,
+                                                uint32_t k) {
+        f.codes[u] = *reinterpret_cast<const u32x2*>(b.w + (row * row_bytes(K) + k / 2));
     }
-    static __device__ __forceinline__ bf16x8 values(const Frag& f) {
-        const float s = scale_value(f.scale);
-        const bf16x2 a = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(f.codes, s, 0);
-        const bf16x2 b = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(f.codes, s, 1);
-        const bf16x2 c = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(f.codes, s, 2);
-        const bf16x2 d = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(f.codes, s, 3);
+    template <int U>
+    static __device__ __forceinline__ void clear(Rows<U>& f, int u) {
+        f.codes[u] = u32x2{0u, 0u};
+    }
+    template <int u, int M, int U>
+    static __device__ __forceinline__ bf16x8 values(const Rows<U>& f) {
+        // quad_perm [0, 0, 2, 2] or [1, 1, 3, 3]
+        const float s = __builtin_bit_cast(float, dpp<u % 2 == 0 ? 0xA0 : 0xF5>(f.scale[u / 2]));
+        const uint32_t v = f.codes[u][M];
+        const bf16x2 a = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(v, s, 0);
+        const bf16x2 b = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(v, s, 1);
+        const bf16x2 c = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(v, s, 2);
+        const bf16x2 d = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(v, s, 3);
         return bf16x8{a[0], a[1], b[0], b[1], c[0], c[1], d[0], d[1]};
     }
 };
 
+template <class W>
+__device__ __forceinline__ int steps_of(int K) {
+    return (K + W::STEP - 1) / W::STEP;
+}
+
+template <int N, class F>
+__device__ __forceinline__ void unrolled(F&& f) {
+    if constexpr (N > 0) {
+        unrolled<N - 1>(f);
+        f(std::integral_constant<int, N - 1>{});
+    }
+}
+
 // acc[r][c] += the lane's row of base[r] (row[r], counted from base[r]) times
 // its column c (first bf16 at x + col[c], in bytes) over the steps [s0, s1) of
-// K.  U steps' loads are issued together; steps past the range repeat the last
-// one's loads (addresses stay inside the row) and are not multiplied.  In a
-// step that K ends inside, lanes past K hold zeros.
+// K, both uniform.  The loads of U steps are in flight: a step's registers are
+// loaded again, for the step U later, as soon as it is multiplied.  In a step
+// that K ends inside, lanes past K load the row's last piece and hold zeros.
 template <class W, int RT, int NT, int U>
 __device__ __forceinline__ void multiply_rows(const WeightBase (&base)[RT], const uint32_t (&row)[RT],
                                               const uint8_t* x, const uint32_t (&col)[NT], int K, int s0, int s1,
                                               f32x4 (&acc)[RT][NT]) {
+    constexpr int PIECE = W::STEP / 16;
+    static_assert(PIECE == 8 * W::SUB && U % W::SCALE_STEPS == 0, "whole pieces, whole scale loads");
     const uint32_t lane = threadIdx.x % kWave;
-    const uint32_t piece = lane / 16 * 32 + lane % 4 * 8;
-    const uint32_t last = (uint32_t)K - 8;
-    for (int s = s0; s < s1; s += U) {
-        typename W::Frag a[U][RT];
-        u32x4 b[U][NT];
+    const uint32_t piece = (lane / 16 * 4 + lane % 4) * PIECE;
+    const uint32_t last = (uint32_t)K - PIECE;
+    typename W::template Rows<U> a[RT];
+    u32x4 b[U][NT][W::SUB];
+    const auto load = [&](auto index, int s) {
+        constexpr int u = decltype(index)::value;
+        const uint32_t k = min((uint32_t)s * W::STEP + piece, last);
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const uint32_t k = min((uint32_t)min(s + u, s1 - 1) * kStep + piece, last);
+        for (int r = 0; r < RT; ++r) W::load(a[r], u, base[r], row[r], K, k);
 #pragma unroll
-            for (int r = 0; r < RT; ++r) a[u][r] = W::load(base[r], row[r], K, k);
+        for (int c = 0; c < NT; ++c)
 #pragma unroll
-            for (int c = 0; c < NT; ++c) b[u][c] = *reinterpret_cast<const u32x4*>(x + (col[c] + k * 2));
-        }
+            for (int m = 0; m < W::SUB; ++m)
+                b[u][c][m] = *reinterpret_cast<const u32x4*>(x + (col[c] + k * 2 + m * 16));
+    };
+    const auto scales = [&](int g, int s) {
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            if (s + u >= s1) continue;  // uniform
-            if ((s + u + 1) * kStep > K && (uint32_t)(s + u) * kStep + piece > last) {
+        for (int r = 0; r < RT; ++r) W::scales(a[r], g, base[r], row[r], K, s);
+    };
+    unrolled<U>([&](auto index) {
+        constexpr int u = decltype(index)::value;
+        if (s0 + u >= s1) return;
+        if constexpr (W::SCALE_STEPS > 1 && u % W::SCALE_STEPS == 0) scales(u / W::SCALE_STEPS, s0 + u);
+        load(index, s0 + u);
+    });
+    for (int s = s0; s < s1; s += U)
+        unrolled<U>([&](auto index) {
+            constexpr int u = decltype(index)::value;
+            if (s + u >= s1) return;
+            if ((s + u + 1) * W::STEP > K && (uint32_t)(s + u) * W::STEP + piece > last) {
 #pragma unroll
-                for (int r = 0; r < RT; ++r) a[u][r] = W::zero();
-#pragma unroll
-                for (int c = 0; c < NT; ++c) b[u][c] = u32x4{0u, 0u, 0u, 0u};
-            }
-#pragma unroll
-            for (int r = 0; r < RT; ++r) {
-                const bf16x8 av = W::values(a[u][r]);
+                for (int r = 0; r < RT; ++r) W::clear(a[r], u);
 #pragma unroll
                 for (int c = 0; c < NT; ++c)
-                    acc[r][c] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(av, __builtin_bit_cast(bf16x8, b[u][c]),
-                                                                        acc[r][c], 0, 0, 0);
+#pragma unroll
+                    for (int m = 0; m < W::SUB; ++m) b[u][c][m] = u32x4{0u, 0u, 0u, 0u};
             }
-        }
-    }
+            unrolled<W::SUB>([&](auto sub) {
+                constexpr int m = decltype(sub)::value;
+#pragma unroll
+                for (int r = 0; r < RT; ++r) {
+                    const bf16x8 av = W::template values<u, m>(a[r]);
+#pragma unroll
+                    for (int c = 0; c < NT; ++c)
+                        acc[r][c] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+                            av, __builtin_bit_cast(bf16x8, b[u][c][m]), acc[r][c], 0, 0, 0);
+                }
+            });
+            if (s + u + U < s1) load(index, s + u + U);
+            if constexpr (W::SCALE_STEPS > 1 && u % W::SCALE_STEPS == W::SCALE_STEPS - 1) {
+                constexpr int first = u - (W::SCALE_STEPS - 1);
+                if (s + first + U < s1) scales(first / W::SCALE_STEPS, s + first + U);
+            }
+        });
 }
 
 // The product of row l / 16 with column l % 16 / 4, in all four lanes of the
