@@ -71,7 +71,7 @@ template <>
 constexpr int kWaveQuads<Mxfp4Weights> = 2;
 // Steps of loads in flight for a task of RT row and NT column tiles.
 template <class W, int RT, int NT>
-constexpr int kInFlight = NT == 1 ? 6 : NT == 2 ? 4 : 2;
+constexpr int kInFlight = NT <= 2 ? 4 : 2;
 template <int RT, int NT>
 constexpr int kInFlight<Mxfp4Weights, RT, NT> = NT == 1 ? 4 : 2;
 
@@ -87,27 +87,34 @@ struct GateUpTask {
 // g, u: the products of QT row quads with the task's tokens over the steps
 // [s0, s1), row l / 16 and column l % 16 / 4 of each tile in lane l.
 template <class W, int QT, int NT>
-__device__ __forceinline__ void gate_up_product(const GateUpTask& t, const uint8_t* x, int H, const uint8_t* w,
+__device__ __forceinline__ void gate_up_product(const GateUpTask& t, __amdgpu_buffer_rsrc_t x, int H, const uint8_t* w,
                                                 const uint8_t* sc, int I, int s0, int s1, float (&g)[QT][NT],
                                                 float (&u)[QT][NT]) {
     const int lane = (int)(threadIdx.x % kWave);
     const size_t first = (size_t)t.e * 2 * I + t.quad * 4;
-    const WeightBase gate{w + uniform_offset(first * W::row_bytes(H)), sc + uniform_offset(first * W::row_scales(H))};
-    const WeightBase up{gate.w + (size_t)I * W::row_bytes(H), gate.scales + (size_t)I * W::row_scales(H)};
-    WeightBase base[2 * QT];
-    uint32_t row[2 * QT], col[NT];
+    const uint32_t row_bytes = W::bytes_of((uint32_t)H), row_scales = W::row_scales(H);
+    const uint8_t* gate = w + uniform_offset(first * row_bytes);
+    const uint8_t* gate_scales = sc + uniform_offset(first * row_scales);
+    // tile 2 q: the gate rows of quad q, tile 2 q + 1: its up rows
+    RowTiles<2 * QT> rows;
+    uint32_t col[NT];
     f32x4 acc[2 * QT][NT];
 #pragma unroll
     for (int r = 0; r < 2 * QT; ++r) {
-        base[r] = r % 2 == 0 ? gate : up;
-        row[r] = (uint32_t)(r / 2 * 4 + lane % 16 / 4);
+        rows.at[r] = (uint32_t)(r / 2 * 4) * row_bytes;
+        rows.scales[r] = gate_scales + ((size_t)(r % 2) * I + r / 2 * 4) * row_scales;
+        rows.last[r] = 3;
 #pragma unroll
         for (int c = 0; c < NT; ++c) acc[r][c] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
     }
 #pragma unroll
-    for (int c = 0; c < NT; ++c)
-        col[c] = (uint32_t)select_bit(t.mask, t.c0 + min(c * 4 + lane % 16 / 4, t.m - 1)) * (uint32_t)H * 2;
-    multiply_rows<W, 2 * QT, NT, kInFlight<W, 2 * QT, NT>>(base, row, x, col, H, s0, s1, acc);
+    for (int c = 0; c < NT; ++c) {
+        const int column = c * 4 + lane % 16 / 4;
+        col[c] = column < t.m ? (uint32_t)select_bit(t.mask, t.c0 + column) * (uint32_t)H * 2 : kNowhere;
+    }
+    multiply_rows<W, 2 * QT, NT, kInFlight<W, 2 * QT, NT>>(
+        buffer_of(gate, (size_t)(4 * QT) * row_bytes),
+        buffer_of(gate + (size_t)I * row_bytes, (size_t)(4 * QT) * row_bytes), rows, x, col, H, s0, s1, acc);
 #pragma unroll
     for (int q = 0; q < QT; ++q)
 #pragma unroll
@@ -123,7 +130,7 @@ __device__ __forceinline__ uint16_t swiglu_bf16(float g, float u) {
 
 // All of K by one wave: the outputs go straight to act.
 template <class W, int QT, int NT>
-__device__ __forceinline__ void gate_up_whole(const GateUpTask& t, const uint8_t* x, int H, const uint8_t* w,
+__device__ __forceinline__ void gate_up_whole(const GateUpTask& t, __amdgpu_buffer_rsrc_t x, int H, const uint8_t* w,
                                               const uint8_t* sc, int I, uint16_t* __restrict__ act) {
     float g[QT][NT], u[QT][NT];
     gate_up_product<W, QT, NT>(t, x, H, w, sc, I, 0, steps_of<W>(H), g, u);
@@ -142,7 +149,7 @@ __device__ __forceinline__ void gate_up_whole(const GateUpTask& t, const uint8_t
 constexpr int kPartSums = 4 * 2 * 16;
 
 template <class W, int NT>
-__device__ __forceinline__ void gate_up_part(const GateUpTask& t, const uint8_t* x, int H, const uint8_t* w,
+__device__ __forceinline__ void gate_up_part(const GateUpTask& t, __amdgpu_buffer_rsrc_t x, int H, const uint8_t* w,
                                              const uint8_t* sc, int I, int s0, int s1, float* sums) {
     float g[1][NT], u[1][NT];
     gate_up_product<W, 1, NT>(t, x, H, w, sc, I, s0, s1, g, u);
@@ -156,7 +163,7 @@ __device__ __forceinline__ void gate_up_part(const GateUpTask& t, const uint8_t*
 }
 
 template <class W, int G, int V>
-__global__ __launch_bounds__(kThreads, 4) void decode_gate_up_kernel(
+__global__ __launch_bounds__(kThreads, 2) void decode_gate_up_kernel(
     const float* __restrict__ logits, const float* __restrict__ bias, int T, int E, int k,
     const uint16_t* __restrict__ x, int H, const uint8_t* __restrict__ w, const uint8_t* __restrict__ sc, int I,
     int32_t* __restrict__ topk_ids, float* __restrict__ topk_weights, Tables* __restrict__ tables,
@@ -222,7 +229,7 @@ __global__ __launch_bounds__(kThreads, 4) void decode_gate_up_kernel(
     }
     const uint32_t per = (uint32_t)I / 4;  // row quads of an expert
     const uint32_t all = uniform((uint32_t)n) * per;
-    const uint8_t* xb = reinterpret_cast<const uint8_t*>(x);
+    const __amdgpu_buffer_rsrc_t xb = buffer_of(x, (size_t)T * H * 2);
     const auto task_of = [&](uint32_t at) {
         GateUpTask t;
         const uint32_t a = at / per;
@@ -289,12 +296,6 @@ __global__ __launch_bounds__(kThreads, 4) void decode_gate_up_kernel(
     }
 }
 
-// Output columns of a workgroup of launch 2, in tiles of 4 rows of w_down.
-template <class W>
-constexpr int kDownTiles = 1;
-template <>
-constexpr int kDownTiles<Mxfp4Weights> = 2;
-
 template <class W, int NT>
 constexpr int kDownInFlight = NT == 1 ? 8 : NT == 2 ? 4 : 2;
 template <int NT>
@@ -311,24 +312,29 @@ __device__ __forceinline__ int k_parts(int n, int pairs) {
     return parts;
 }
 
-template <class W, int NT>
-__device__ __forceinline__ void down_columns(const WeightBase& rows, int left, const uint8_t* act, int I, int p0,
-                                             int end, int s0, int s1, float* y) {
-    constexpr int RT = kDownTiles<W>;
+template <class W, int RT, int NT>
+__device__ __forceinline__ void down_columns(const uint8_t* w, const uint8_t* sc, __amdgpu_buffer_rsrc_t act, int I,
+                                             int p0, int end, int s0, int s1, float* y) {
     const int lane = (int)(threadIdx.x % kWave);
-    WeightBase base[RT];
-    uint32_t row[RT], col[NT];
+    const uint32_t row_bytes = W::bytes_of((uint32_t)I), row_scales = W::row_scales(I);
+    RowTiles<RT> rows;
+    uint32_t col[NT];
     f32x4 acc[RT][NT];
 #pragma unroll
     for (int r = 0; r < RT; ++r) {
-        base[r] = rows;
-        row[r] = (uint32_t)min(r * 4 + lane % 16 / 4, left - 1);
+        rows.at[r] = (uint32_t)(r * 4) * row_bytes;
+        rows.scales[r] = sc + (size_t)(r * 4) * row_scales;
+        rows.last[r] = 3;
 #pragma unroll
         for (int c = 0; c < NT; ++c) acc[r][c] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
     }
 #pragma unroll
-    for (int c = 0; c < NT; ++c) col[c] = (uint32_t)min(p0 + c * 4 + lane % 16 / 4, end - 1) * (uint32_t)I * 2;
-    multiply_rows<W, RT, NT, kDownInFlight<W, NT>>(base, row, act, col, I, s0, s1, acc);
+    for (int c = 0; c < NT; ++c) {
+        const int p = p0 + c * 4 + lane % 16 / 4;
+        col[c] = p < end ? (uint32_t)p * (uint32_t)I * 2 : kNowhere;
+    }
+    const __amdgpu_buffer_rsrc_t wb = buffer_of(w, (size_t)(4 * RT) * row_bytes);
+    multiply_rows<W, RT, NT, kDownInFlight<W, NT>>(wb, wb, rows, act, col, I, s0, s1, acc);
 #pragma unroll
     for (int c = 0; c < NT; ++c) {
         const int p = p0 + c * 4 + lane % 16 / 4;
@@ -340,14 +346,15 @@ __device__ __forceinline__ void down_columns(const WeightBase& rows, int left, c
     }
 }
 
-template <class W>
+// RT tiles of 4 output columns a workgroup; H is a multiple of 4 RT.
+template <class W, int RT>
 __global__ __launch_bounds__(kThreads) void decode_down_kernel(int T, int k, const uint8_t* __restrict__ w,
                                                                const uint8_t* __restrict__ sc, int H, int I,
                                                                const Tables* __restrict__ tables,
                                                                const uint16_t* __restrict__ act,
                                                                const float* __restrict__ topk_weights,
                                                                uint16_t* __restrict__ out) {
-    constexpr int ROWS = 4 * kDownTiles<W>;
+    constexpr int ROWS = 4 * RT;
     __shared__ float s_y[kMaxY * ROWS];  // [part][p][row]
     __shared__ float s_w[kMaxSlots];
     __shared__ int32_t s_dest[kMaxSlots];
@@ -361,20 +368,21 @@ __global__ __launch_bounds__(kThreads) void decode_down_kernel(int T, int k, con
     }
     const int parts = k_parts(n, pairs);
     const int steps = steps_of<W>(I);
-    const uint8_t* actb = reinterpret_cast<const uint8_t*>(act);
+    const __amdgpu_buffer_rsrc_t actb = buffer_of(act, (size_t)pairs * I * 2);
     for (int task = wave; task < n * parts; task += kWaves) {
         const int a = task / parts, part = task - a * parts;
         const size_t row = (size_t)tables->expert[a] * H + h0;
-        const WeightBase rows{w + uniform_offset(row * W::row_bytes(I)), sc + uniform_offset(row * W::row_scales(I))};
+        const uint8_t* rw = w + uniform_offset(row * W::bytes_of((uint32_t)I));
+        const uint8_t* rs = sc + uniform_offset(row * W::row_scales(I));
         const int begin = tables->first[a], end = tables->first[a + 1];
         const int s0 = steps * part / parts, s1 = steps * (part + 1) / parts;
         float* y = s_y + part * pairs * ROWS;
         if (end - begin <= 4)
-            down_columns<W, 1>(rows, H - h0, actb, I, begin, end, s0, s1, y);
+            down_columns<W, RT, 1>(rw, rs, actb, I, begin, end, s0, s1, y);
         else if (end - begin <= 8 || kEntryTokens<W> == 8)
-            down_columns<W, 2>(rows, H - h0, actb, I, begin, end, s0, s1, y);
+            down_columns<W, RT, 2>(rw, rs, actb, I, begin, end, s0, s1, y);
         else if constexpr (kEntryTokens<W> == 16)
-            down_columns<W, 4>(rows, H - h0, actb, I, begin, end, s0, s1, y);
+            down_columns<W, RT, 4>(rw, rs, actb, I, begin, end, s0, s1, y);
     }
     __syncthreads();
     for (int i = (int)threadIdx.x; i < T * ROWS; i += kThreads) {
@@ -386,11 +394,13 @@ __global__ __launch_bounds__(kThreads) void decode_down_kernel(int T, int k, con
             for (int part = 0; part < parts; ++part) y += s_y[(part * pairs + s_dest[s]) * ROWS + h];
             sum = fmaf(s_w[s], y, sum);
         }
-        if (h0 + h < H) out[(size_t)t * H + h0 + h] = (uint16_t)(pack_bf16x2(sum, 0.0f) & 0xFFFFu);
+        out[(size_t)t * H + h0 + h] = (uint16_t)(pack_bf16x2(sum, 0.0f) & 0xFFFFu);
     }
 }
 
-constexpr int kMaxGrid = 512;  // two workgroups per CU
+constexpr int kWideDown = 3584;
+
+constexpr int kMaxGrid = 256;  // one workgroup per CU: 8 waves with up to 256 registers each
 
 template <class W, int G, int V>
 hipError_t launch_gv(const DecodeLayerArgs& a, hipStream_t stream) {
@@ -404,10 +414,19 @@ hipError_t launch_gv(const DecodeLayerArgs& a, hipStream_t stream) {
         a.topk_ids, a.topk_weights, tables, act);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
-    decode_down_kernel<W><<<(a.H + 4 * kDownTiles<W> - 1) / (4 * kDownTiles<W>), kThreads, 0, stream>>>(
-        a.T, a.k, static_cast<const uint8_t*>(a.w_down), a.s_down, a.H, a.I, tables, act, a.topk_weights,
-        static_cast<uint16_t*>(a.out));
-    return hipGetLastError();
+    const auto down = [&](auto tiles) {
+        constexpr int RT = decltype(tiles)::value;
+        decode_down_kernel<W, RT><<<a.H / (4 * RT), kThreads, 0, stream>>>(
+            a.T, a.k, static_cast<const uint8_t*>(a.w_down), a.s_down, a.H, a.I, tables, act, a.topk_weights,
+            static_cast<uint16_t*>(a.out));
+        return hipGetLastError();
+    };
+    if constexpr (std::is_same_v<W, Bf16Weights>)
+        return down(std::integral_constant<int, 1>{});
+    else if (a.H >= kWideDown)
+        return down(std::integral_constant<int, 4>{});
+    else
+        return down(std::integral_constant<int, 2>{});
 }
 
 template <class W>

@@ -25,22 +25,28 @@ __global__ __launch_bounds__(kThreads) void linear_mxfp4_kernel(const uint16_t* 
     const int wave = wave_index();
     const int n0 = (int)blockIdx.x * (4 * kTiles);
     const int c0 = (int)blockIdx.y * (4 * NT);
-    const WeightBase rows{w + (size_t)n0 * W::row_bytes(K), sc + (size_t)n0 * W::row_scales(K)};
-    WeightBase base[kTiles];
-    uint32_t row[kTiles], col[NT];
+    const uint32_t row_bytes = W::bytes_of((uint32_t)K), row_scales = W::row_scales(K);
+    RowTiles<kTiles> rows;
+    uint32_t col[NT];
     f32x4 acc[kTiles][NT];
 #pragma unroll
     for (int r = 0; r < kTiles; ++r) {
-        base[r] = rows;
-        row[r] = (uint32_t)min(r * 4 + lane % 16 / 4, N - 1 - n0);
+        const int first = min(r * 4, N - 1 - n0);  // a tile past W: its last row
+        rows.at[r] = (uint32_t)first * row_bytes;
+        rows.scales[r] = sc + (size_t)(n0 + first) * row_scales;
+        rows.last[r] = (uint32_t)min(3, N - 1 - n0 - first);
 #pragma unroll
         for (int c = 0; c < NT; ++c) acc[r][c] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
     }
 #pragma unroll
-    for (int c = 0; c < NT; ++c) col[c] = (uint32_t)min(c0 + c * 4 + lane % 16 / 4, T - 1) * (uint32_t)K * 2;
+    for (int c = 0; c < NT; ++c) {
+        const int t = c0 + c * 4 + lane % 16 / 4;
+        col[c] = t < T ? (uint32_t)t * (uint32_t)K * 2 : kNowhere;
+    }
     const int steps = steps_of<W>(K);
-    multiply_rows<W, kTiles, NT, (NT == 4 ? 2 : 4)>(base, row, reinterpret_cast<const uint8_t*>(x), col, K, steps * wave / kWaves,
-                                    steps * (wave + 1) / kWaves, acc);
+    const __amdgpu_buffer_rsrc_t wb = buffer_of(w + (size_t)n0 * row_bytes, (size_t)(N - n0) * row_bytes);
+    multiply_rows<W, kTiles, NT, (NT == 4 ? 2 : 4)>(wb, wb, rows, buffer_of(x, (size_t)T * K * 2), col, K,
+                                                    steps * wave / kWaves, steps * (wave + 1) / kWaves, acc);
 #pragma unroll
     for (int c = 0; c < NT; ++c)
 #pragma unroll
