@@ -296,10 +296,11 @@ __global__ __launch_bounds__(kThreads, 2) void decode_gate_up_kernel(
     }
 }
 
-template <class W, int NT>
+// Steps of loads in flight for RT row and NT column tiles.
+template <class W, int RT, int NT>
 constexpr int kDownInFlight = NT == 1 ? 8 : NT == 2 ? 4 : 2;
-template <int NT>
-constexpr int kDownInFlight<Mxfp4Weights, NT> = NT == 1 ? 4 : 2;
+template <int RT, int NT>
+constexpr int kDownInFlight<Mxfp4Weights, RT, NT> = NT == 1 || RT == 4 ? 4 : 2;
 
 constexpr int kMaxY = kMaxSlots;  // y entries of a workgroup: pairs times K parts
 
@@ -334,7 +335,7 @@ __device__ __forceinline__ void down_columns(const uint8_t* w, const uint8_t* sc
         col[c] = p < end ? (uint32_t)p * (uint32_t)I * 2 : kNowhere;
     }
     const __amdgpu_buffer_rsrc_t wb = buffer_of(w, (size_t)(4 * RT) * row_bytes);
-    multiply_rows<W, RT, NT, kDownInFlight<W, NT>>(wb, wb, rows, act, col, I, s0, s1, acc);
+    multiply_rows<W, RT, NT, kDownInFlight<W, RT, NT>>(wb, wb, rows, act, col, I, s0, s1, acc);
 #pragma unroll
     for (int c = 0; c < NT; ++c) {
         const int p = p0 + c * 4 + lane % 16 / 4;
@@ -426,7 +427,7 @@ hipError_t launch_gv(const DecodeLayerArgs& a, hipStream_t stream) {
     else if (a.H >= kWideDown)
         return down(std::integral_constant<int, 4>{});
     else
-        return down(std::integral_constant<int, 2>{});
+        return down(std::integral_constant<int, 1>{});
 }
 
 template <class W>

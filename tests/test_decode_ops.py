@@ -225,7 +225,9 @@ def test_linear_mxfp4_every_code_and_scale(dev):
 
 @pytest.mark.parametrize("T,K,N", [(1, 32, 1), (1, 64, 17), (2, 96, 5), (5, 128, 33), (16, 160, 16), (17, 256, 15),
                                    (31, 2048, 70), (33, 1056, 31), (48, 992, 64), (64, 7168, 50), (64, 4096, 130),
-                                   (1, 7168, 4096), (7, 16384, 19)])
+                                   (1, 7168, 4096), (7, 16384, 19), (20, 96, 4097), (40, 1312, 5000), (9, 288, 4104),
+                                   (5, 544, 8196), (33, 160, 8193), (64, 2016, 1030), (17, 256, 1028), (12, 32, 6001),
+                                   (64, 4128, 8200)])
 def test_linear_mxfp4(dev, T, K, N):
     import torch
     import moe_glue_amd as mg
