@@ -40,15 +40,21 @@ __all__ = ["route", "route_workspace_bytes", "alloc_route_outputs", "route_padde
            "NORM_H_MAX", "DECODE_T_MAX"]
 
 
-def _torch():
-    import torch
+_torch_module = None
 
-    return torch
+
+def _torch():
+    global _torch_module
+    if _torch_module is None:
+        import torch
+
+        _torch_module = torch
+    return _torch_module
 
 
 def _stream(device) -> int:
-    torch = _torch()
-    return torch.cuda.current_stream(device).cuda_stream
+    """Handle of torch's current stream on `device`."""
+    return _torch()._C._cuda_getCurrentRawStream(device.index)
 
 
 def _ptr(t) -> int:
@@ -467,10 +473,12 @@ def _enqueue(fn: str, device, *args) -> None:
     torch = _torch()
     call = getattr(load(), fn)
     if torch.cuda.current_device() == device.index:
-        check(call(*args, _stream(device)), fn)
-        return
-    with torch.cuda.device(device):
-        check(call(*args, _stream(device)), fn)
+        status = call(*args, _stream(device))
+    else:
+        with torch.cuda.device(device):
+            status = call(*args, _stream(device))
+    if status:
+        check(status, fn)
 
 
 def _norm_args(x, weight, residual, residual_out, out, normed_name: str):
@@ -574,16 +582,20 @@ def _decode_args(logits, k: int, x, w_gate_up, w_down, bias, out, mx: bool):
     dev = x.device
     if x.shape[0] != T:
         raise MoEGlueArgumentError(2, f"x has {x.shape[0]} rows, logits has T={T}")
-    _same_device([("logits", logits), ("bias", bias)], dev)
+    if logits.device != dev or (bias is not None and bias.device != dev):
+        _same_device([("logits", logits), ("bias", bias)], dev)
     _check_bias(bias, E)
-    dtype = torch.uint8 if mx else torch.bfloat16
-    _need_gpu("w_gate_up", w_gate_up, dtype, 3)
+    if w_gate_up is None or w_gate_up.dim() != 3:
+        _need_gpu("w_gate_up", w_gate_up, None, 3)
     I = w_gate_up.shape[1] // 2
-    pack = 2 if mx else 1
-    if mx and (H % 32 != 0 or I % 32 != 0):
-        raise MoEGlueArgumentError(2, f"H={H} and I={I} must be multiples of the 32-column block")
-    _check_shape("w_gate_up", w_gate_up, dtype, (E, 2 * I, H // pack), dev)
-    _check_shape("w_down", w_down, dtype, (E, H, I // pack), dev)
+    if mx:
+        if H % 32 != 0 or I % 32 != 0:
+            raise MoEGlueArgumentError(2, f"H={H} and I={I} must be multiples of the 32-column block")
+        _check_shape("w_gate_up", w_gate_up, torch.uint8, (E, 2 * I, H // 2), dev)
+        _check_shape("w_down", w_down, torch.uint8, (E, H, I // 2), dev)
+    else:
+        _check_shape("w_gate_up", w_gate_up, torch.bfloat16, (E, 2 * I, H), dev)
+        _check_shape("w_down", w_down, torch.bfloat16, (E, H, I), dev)
     if out is None:
         if not 0 < k <= min(E, K_MAX):
             raise MoEGlueArgumentError(2, f"k={k} must be in [1, {min(E, K_MAX)}]")
@@ -593,8 +605,9 @@ def _decode_args(logits, k: int, x, w_gate_up, w_down, bias, out, mx: bool):
         _check_shape("topk_weights", out.get("topk_weights"), torch.float32, (T, k), dev)
         _check_shape("out", out.get("out"), torch.bfloat16, (T, H), dev)
         ws = out.get("workspace")
-        _need_gpu("workspace", ws, torch.uint8)
-        _same_device([("workspace", ws)], dev)
+        if ws is None or ws.device != dev or ws.dtype != torch.uint8 or not ws.is_contiguous():
+            _need_gpu("workspace", ws, torch.uint8)
+            _same_device([("workspace", ws)], dev)
     return T, E, H, I, out
 
 
@@ -605,9 +618,9 @@ def decode_layer(logits, k: int, x, w_gate_up, w_down, bias=None, out: dict | No
     the workspace.  See moe_decode_layer in include/moe_glue.h."""
     T, E, H, I, out = _decode_args(logits, k, x, w_gate_up, w_down, bias, out, False)
     ws = out["workspace"]
-    _enqueue("moe_decode_layer", x.device, _ptr(logits), _ptr(bias), T, E, k, _ptr(x), H, _ptr(w_gate_up),
-             _ptr(w_down), I, _ptr(out["topk_ids"]), _ptr(out["topk_weights"]), _ptr(out["out"]), _ptr(ws),
-             ws.numel())
+    _enqueue("moe_decode_layer", x.device, logits.data_ptr(), _ptr(bias), T, E, k, x.data_ptr(), H,
+             w_gate_up.data_ptr(), w_down.data_ptr(), I, out["topk_ids"].data_ptr(), out["topk_weights"].data_ptr(),
+             out["out"].data_ptr(), ws.data_ptr(), ws.numel())
     return out
 
 
@@ -622,9 +635,10 @@ def decode_layer_mxfp4(logits, k: int, x, w_gate_up, s_gate_up, w_down, s_down, 
     _check_shape("s_gate_up", s_gate_up, u8, (E, 2 * I, H // 32), x.device)
     _check_shape("s_down", s_down, u8, (E, H, I // 32), x.device)
     ws = out["workspace"]
-    _enqueue("moe_decode_layer_mxfp4", x.device, _ptr(logits), _ptr(bias), T, E, k, _ptr(x), H, _ptr(w_gate_up),
-             _ptr(s_gate_up), _ptr(w_down), _ptr(s_down), I, _ptr(out["topk_ids"]), _ptr(out["topk_weights"]),
-             _ptr(out["out"]), _ptr(ws), ws.numel())
+    _enqueue("moe_decode_layer_mxfp4", x.device, logits.data_ptr(), _ptr(bias), T, E, k, x.data_ptr(), H,
+             w_gate_up.data_ptr(), s_gate_up.data_ptr(), w_down.data_ptr(), s_down.data_ptr(), I,
+             out["topk_ids"].data_ptr(), out["topk_weights"].data_ptr(), out["out"].data_ptr(), ws.data_ptr(),
+             ws.numel())
     return out
 
 
@@ -637,7 +651,8 @@ def linear_mxfp4(x, w, scales, out=None):
     T, K = x.shape
     if K % 32 != 0:
         raise MoEGlueArgumentError(2, f"K={K} is not a multiple of the 32-column block")
-    _need_gpu("w", w, torch.uint8, 2)
+    if w is None or w.dim() != 2:
+        _need_gpu("w", w, None, 2)
     N = w.shape[0]
     _check_shape("w", w, torch.uint8, (N, K // 2), x.device)
     _check_shape("scales", scales, torch.uint8, (N, K // 32), x.device)
@@ -645,7 +660,7 @@ def linear_mxfp4(x, w, scales, out=None):
         out = torch.empty((T, N), dtype=torch.bfloat16, device=x.device)
     else:
         _check_shape("out", out, torch.bfloat16, (T, N), x.device)
-    _enqueue("moe_linear_mxfp4", x.device, _ptr(x), T, K, _ptr(w), _ptr(scales), N, _ptr(out))
+    _enqueue("moe_linear_mxfp4", x.device, x.data_ptr(), T, K, w.data_ptr(), scales.data_ptr(), N, out.data_ptr())
     return out
 
 
