@@ -46,6 +46,12 @@ constexpr int kEntryTokens = 16;
 template <>
 constexpr int kEntryTokens<Mxfp4Weights> = 8;  // by registers, see mfma_rows.h
 constexpr int kMaxEntries = kEMax + kMaxSlots / 8;
+// Weights are streamed past the caches (decode workload 132 -> 120 and 65 -> 61
+// us, DeepSeek-V3-shaped MXFP4 247 -> 234 and 134 -> 129), except under entries
+// as wide as they come: the expert may have another, which reads them again
+// (skewed MXFP4 98 -> 86 and 55 -> 52).
+template <class W, int NT>
+constexpr int kWeightCache = NT * 4 < kEntryTokens<W> ? kCacheNt : 0;
 
 // Front of the workspace, written by launch 1 for launch 2.
 struct Tables {
@@ -112,7 +118,7 @@ __device__ __forceinline__ void gate_up_product(const GateUpTask& t, __amdgpu_bu
         const int column = c * 4 + lane % 16 / 4;
         col[c] = column < t.m ? (uint32_t)select_bit(t.mask, t.c0 + column) * (uint32_t)H * 2 : kNowhere;
     }
-    multiply_rows<W, 2 * QT, NT, kInFlight<W, 2 * QT, NT>>(
+    multiply_rows<W, 2 * QT, NT, kInFlight<W, 2 * QT, NT>, kWeightCache<W, NT>>(
         buffer_of(gate, (size_t)(4 * QT) * row_bytes),
         buffer_of(gate + (size_t)I * row_bytes, (size_t)(4 * QT) * row_bytes), rows, x, col, H, s0, s1, acc);
 #pragma unroll
@@ -335,7 +341,7 @@ __device__ __forceinline__ void down_columns(const uint8_t* w, const uint8_t* sc
         col[c] = p < end ? (uint32_t)p * (uint32_t)I * 2 : kNowhere;
     }
     const __amdgpu_buffer_rsrc_t wb = buffer_of(w, (size_t)(4 * RT) * row_bytes);
-    multiply_rows<W, RT, NT, kDownInFlight<W, RT, NT>>(wb, wb, rows, act, col, I, s0, s1, acc);
+    multiply_rows<W, RT, NT, kDownInFlight<W, RT, NT>, kWeightCache<W, NT>>(wb, wb, rows, act, col, I, s0, s1, acc);
 #pragma unroll
     for (int c = 0; c < NT; ++c) {
         const int p = p0 + c * 4 + lane % 16 / 4;

@@ -49,8 +49,9 @@ __global__ __launch_bounds__(kThreads, NT == 1 ? 4 : 2) void linear_mxfp4_kernel
     }
     const int steps = steps_of<W>(K);
     const __amdgpu_buffer_rsrc_t wb = buffer_of(w + (size_t)n0 * row_bytes, (size_t)(N - n0) * row_bytes);
-    multiply_rows<W, kTiles, NT, (NT == 2 ? 4 : 2)>(wb, wb, rows, buffer_of(x, (size_t)T * K * 2), col, K,
-                                                    steps * wave / kWaves, steps * (wave + 1) / kWaves, acc);
+    multiply_rows<W, kTiles, NT, (NT == 2 ? 4 : 2), kCacheNt>(wb, wb, rows, buffer_of(x, (size_t)T * K * 2), col, K,
+                                                              steps * wave / kWaves,
+                                                              steps * (wave + 1) / kWaves, acc);
 #pragma unroll
     for (int c = 0; c < NT; ++c)
 #pragma unroll

@@ -56,7 +56,7 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer_of(const void* p, size_
 }
 
 // A lane's part of one row in a step (Frag), and what its tile's rows carry
-// over several steps (Scales).  Weights are streamed: non-temporal loads.
+// over several steps (Scales).
 struct Bf16Weights {
     static constexpr int STEP = 128;
     static constexpr int SUB = 1;          // MFMAs per step
@@ -65,8 +65,9 @@ struct Bf16Weights {
     struct Scales {};
     static __host__ __device__ __forceinline__ uint32_t bytes_of(uint32_t k) { return k * 2; }
     static __host__ __device__ __forceinline__ uint32_t row_scales(int) { return 0; }
+    template <int CACHE>
     static __device__ __forceinline__ Frag load(__amdgpu_buffer_rsrc_t w, uint32_t lane, uint32_t step) {
-        return __builtin_bit_cast(Frag, __builtin_amdgcn_raw_buffer_load_b128(w, (int)lane, (int)step, kCacheNt));
+        return __builtin_bit_cast(Frag, __builtin_amdgcn_raw_buffer_load_b128(w, (int)lane, (int)step, CACHE));
     }
     template <int M>
     static __device__ __forceinline__ bf16x8 values(const Frag& f, float) {
@@ -90,8 +91,9 @@ struct Mxfp4Weights {
     };
     static __host__ __device__ __forceinline__ uint32_t bytes_of(uint32_t k) { return k / 2; }
     static __host__ __device__ __forceinline__ uint32_t row_scales(int K) { return (uint32_t)K / 32; }
+    template <int CACHE>
     static __device__ __forceinline__ Frag load(__amdgpu_buffer_rsrc_t w, uint32_t lane, uint32_t step) {
-        return __builtin_bit_cast(Frag, __builtin_amdgcn_raw_buffer_load_b64(w, (int)lane, (int)step, kCacheNt));
+        return __builtin_bit_cast(Frag, __builtin_amdgcn_raw_buffer_load_b64(w, (int)lane, (int)step, CACHE));
     }
     // The lane's four scale bytes of the 8 steps from `step` on, of the row whose
     // scales begin at p + row, in one dword at any byte address; at a row's end
@@ -162,8 +164,9 @@ struct RowTiles {
 // uniform.  col[c]: the byte offset of the lane's column in x, or kNowhere.
 // The loads of U steps are in flight: a step's registers are loaded again, for
 // the step U later, as soon as it is multiplied.  In a step that K ends inside,
-// lanes past K hold zeros.
-template <class W, int RT, int NT, int U>
+// lanes past K hold zeros.  CACHE: the weight loads' cache bits, kCacheNt where
+// no other wave will read them.
+template <class W, int RT, int NT, int U, int CACHE>
 __device__ __forceinline__ void multiply_rows(__amdgpu_buffer_rsrc_t w0, __amdgpu_buffer_rsrc_t w1,
                                               const RowTiles<RT>& rows, __amdgpu_buffer_rsrc_t x,
                                               const uint32_t (&col)[NT], int K, int s0, int s1,
@@ -191,7 +194,8 @@ __device__ __forceinline__ void multiply_rows(__amdgpu_buffer_rsrc_t w0, __amdgp
         const bool past = !whole && s == partial && k + piece >= (uint32_t)K;
 #pragma unroll
         for (int r = 0; r < RT; ++r)
-            a[u][r] = W::load(r % 2 == 0 ? w0 : w1, past ? kNowhere : a_at[r], rows.at[r] + W::bytes_of(k));
+            a[u][r] = W::template load<CACHE>(r % 2 == 0 ? w0 : w1, past ? kNowhere : a_at[r],
+                                              rows.at[r] + W::bytes_of(k));
 #pragma unroll
         for (int c = 0; c < NT; ++c)
 #pragma unroll
