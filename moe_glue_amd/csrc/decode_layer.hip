@@ -103,7 +103,7 @@ __device__ __forceinline__ void gate_up_product(const GateUpTask& t, __amdgpu_bu
     const uint8_t* gate_scales = sc + uniform_offset(first * row_scales);
     // tile 2 q: the gate rows of quad q, tile 2 q + 1: its up rows
     RowTiles<2 * QT> rows;
-    uint32_t col[NT];
+    uint32_t col[1][NT];
     f32x4 acc[2 * QT][NT];
 #pragma unroll
     for (int r = 0; r < 2 * QT; ++r) {
@@ -116,9 +116,9 @@ __device__ __forceinline__ void gate_up_product(const GateUpTask& t, __amdgpu_bu
 #pragma unroll
     for (int c = 0; c < NT; ++c) {
         const int column = c * 4 + lane % 16 / 4;
-        col[c] = column < t.m ? (uint32_t)select_bit(t.mask, t.c0 + column) * (uint32_t)H * 2 : kNowhere;
+        col[0][c] = column < t.m ? (uint32_t)select_bit(t.mask, t.c0 + column) * (uint32_t)H * 2 : kNowhere;
     }
-    multiply_rows<W, 2 * QT, NT, kInFlight<W, 2 * QT, NT>, kWeightCache<W, NT>>(
+    multiply_rows<W, 2 * QT, NT, kInFlight<W, 2 * QT, NT>, kWeightCache<W, NT>, 1>(
         buffer_of(gate, (size_t)(4 * QT) * row_bytes),
         buffer_of(gate + (size_t)I * row_bytes, (size_t)(4 * QT) * row_bytes), rows, x, col, H, s0, s1, acc);
 #pragma unroll
@@ -319,42 +319,53 @@ __device__ __forceinline__ int k_parts(int n, int pairs) {
     return parts;
 }
 
-template <class W, int RT, int NT>
-__device__ __forceinline__ void down_columns(const uint8_t* w, const uint8_t* sc, __amdgpu_buffer_rsrc_t act, int I,
-                                             int p0, int end, int s0, int s1, float* y) {
+// What a task of launch 2 multiplies: the rows of w_down from w on by the act
+// rows p0 to end - 1.
+struct DownTask {
+    const uint8_t* w;
+    const uint8_t* scales;
+    int p0, end;
+};
+
+// G tasks side by side (G = 1, or 2 with the same s0 and s1), RT row tiles each.
+template <class W, int RT, int NT, int G>
+__device__ __forceinline__ void down_columns(const DownTask (&t)[G], __amdgpu_buffer_rsrc_t act, int I, int s0,
+                                             int s1, float* y) {
     const int lane = (int)(threadIdx.x % kWave);
     const uint32_t row_bytes = W::bytes_of((uint32_t)I), row_scales = W::row_scales(I);
-    RowTiles<RT> rows;
-    uint32_t col[NT];
-    f32x4 acc[RT][NT];
+    RowTiles<RT * G> rows;  // tile r * G + g: row tile r of task g
+    uint32_t col[G][NT];
+    f32x4 acc[RT * G][NT];
 #pragma unroll
-    for (int r = 0; r < RT; ++r) {
-        rows.at[r] = (uint32_t)(r * 4) * row_bytes;
-        rows.scales[r] = sc + (size_t)(r * 4) * row_scales;
+    for (int r = 0; r < RT * G; ++r) {
+        rows.at[r] = (uint32_t)(r / G * 4) * row_bytes;
+        rows.scales[r] = t[r % G].scales + (size_t)(r / G * 4) * row_scales;
         rows.last[r] = 3;
 #pragma unroll
         for (int c = 0; c < NT; ++c) acc[r][c] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
     }
 #pragma unroll
-    for (int c = 0; c < NT; ++c) {
-        const int p = p0 + c * 4 + lane % 16 / 4;
-        col[c] = p < end ? (uint32_t)p * (uint32_t)I * 2 : kNowhere;
-    }
-    const __amdgpu_buffer_rsrc_t wb = buffer_of(w, (size_t)(4 * RT) * row_bytes);
-    multiply_rows<W, RT, NT, kDownInFlight<W, RT, NT>, kWeightCache<W, NT>>(wb, wb, rows, act, col, I, s0, s1, acc);
+    for (int g = 0; g < G; ++g)
 #pragma unroll
-    for (int c = 0; c < NT; ++c) {
-        const int p = p0 + c * 4 + lane % 16 / 4;
-#pragma unroll
-        for (int r = 0; r < RT; ++r) {
-            const float v = diagonal_sum(acc[r][c]);
-            if (lane % 4 == r && p < end) y[p * (4 * RT) + r * 4 + lane / 16] = v;
+        for (int c = 0; c < NT; ++c) {
+            const int p = t[g].p0 + c * 4 + lane % 16 / 4;
+            col[g][c] = p < t[g].end ? (uint32_t)p * (uint32_t)I * 2 : kNowhere;
         }
-    }
+    const size_t bytes = (size_t)(4 * RT) * row_bytes;
+    multiply_rows<W, RT * G, NT, kDownInFlight<W, RT, NT * G>, kWeightCache<W, NT>, G>(
+        buffer_of(t[0].w, bytes), buffer_of(t[G - 1].w, bytes), rows, act, col, I, s0, s1, acc);
+#pragma unroll
+    for (int c = 0; c < NT; ++c)
+#pragma unroll
+        for (int r = 0; r < RT * G; ++r) {
+            const int p = t[r % G].p0 + c * 4 + lane % 16 / 4;
+            const float v = diagonal_sum(acc[r][c]);
+            if (lane % 4 == r % 4 && p < t[r % G].end) y[p * (4 * RT) + r / G * 4 + lane / 16] = v;
+        }
 }
 
 // RT tiles of 4 output columns a workgroup; H is a multiple of 4 RT.
-template <class W, int RT>
+template <class W, int RT, bool PAIRS>
 __global__ __launch_bounds__(kThreads) void decode_down_kernel(int T, int k, const uint8_t* __restrict__ w,
                                                                const uint8_t* __restrict__ sc, int H, int I,
                                                                const Tables* __restrict__ tables,
@@ -376,20 +387,34 @@ __global__ __launch_bounds__(kThreads) void decode_down_kernel(int T, int k, con
     const int parts = k_parts(n, pairs);
     const int steps = steps_of<W>(I);
     const __amdgpu_buffer_rsrc_t actb = buffer_of(act, (size_t)pairs * I * 2);
+    const auto task_of = [&](int a) {
+        const size_t row = (size_t)tables->expert[a] * H + h0;
+        return DownTask{w + uniform_offset(row * W::bytes_of((uint32_t)I)),
+                        sc + uniform_offset(row * W::row_scales(I)), tables->first[a], tables->first[a + 1]};
+    };
     for (int task = wave; task < n * parts; task += kWaves) {
         const int a = task / parts, part = task - a * parts;
-        const size_t row = (size_t)tables->expert[a] * H + h0;
-        const uint8_t* rw = w + uniform_offset(row * W::bytes_of((uint32_t)I));
-        const uint8_t* rs = sc + uniform_offset(row * W::row_scales(I));
-        const int begin = tables->first[a], end = tables->first[a + 1];
+        const DownTask t[1] = {task_of(a)};
+        // two small entries at a time: a wave with short rows would wait out the
+        // memory's latency after every few loads (MXFP4, 32 tokens, 2048 x 768 38.0
+        // -> 34.2 us, 1024 x 2048 45 -> 40; not for bf16 rows, 58 -> 61 us)
+        if (PAIRS && parts == 1 && task + kWaves < n && t[0].end - t[0].p0 <= 4) {
+            const DownTask two[2] = {t[0], task_of(task + kWaves)};
+            if (two[1].end - two[1].p0 <= 4) {
+                down_columns<W, RT, 1, 2>(two, actb, I, 0, steps, s_y);
+                task += kWaves;
+                continue;
+            }
+        }
+        const int m = t[0].end - t[0].p0;
         const int s0 = steps * part / parts, s1 = steps * (part + 1) / parts;
         float* y = s_y + part * pairs * ROWS;
-        if (end - begin <= 4)
-            down_columns<W, RT, 1>(rw, rs, actb, I, begin, end, s0, s1, y);
-        else if (end - begin <= 8 || kEntryTokens<W> == 8)
-            down_columns<W, RT, 2>(rw, rs, actb, I, begin, end, s0, s1, y);
+        if (m <= 4)
+            down_columns<W, RT, 1, 1>(t, actb, I, s0, s1, y);
+        else if (m <= 8 || kEntryTokens<W> == 8)
+            down_columns<W, RT, 2, 1>(t, actb, I, s0, s1, y);
         else if constexpr (kEntryTokens<W> == 16)
-            down_columns<W, RT, 4>(rw, rs, actb, I, begin, end, s0, s1, y);
+            down_columns<W, RT, 4, 1>(t, actb, I, s0, s1, y);
     }
     __syncthreads();
     for (int i = (int)threadIdx.x; i < T * ROWS; i += kThreads) {
@@ -405,9 +430,17 @@ __global__ __launch_bounds__(kThreads) void decode_down_kernel(int T, int k, con
     }
 }
 
+// From this width on MXFP4's launch 2 takes 16 columns a workgroup instead of 4:
+// four row tiles share a column's loads, which cost more than theirs.  Below, too
+// few workgroups would be left.  One against the other (us): H = 2048 53 / 38,
+// 1024 74 / 45, 3584 33 / 39, 4096 55 / 67, 7168 130 / 146 (the last three against
+// 8 columns).  With bf16 weights 8 columns against 4 changes nothing either way.
 constexpr int kWideDown = 3584;
 
-constexpr int kMaxGrid = 256;  // one workgroup per CU: 8 waves with up to 256 registers each
+// One workgroup per CU, its 8 waves with up to 256 registers each.  Two of half
+// the registers: decode workload 117 -> 121 us, DeepSeek-V3-shaped MXFP4, which
+// then spills, 235 -> 299 us.
+constexpr int kMaxGrid = 256;
 
 template <class W, int G, int V>
 hipError_t launch_gv(const DecodeLayerArgs& a, hipStream_t stream) {
@@ -421,19 +454,19 @@ hipError_t launch_gv(const DecodeLayerArgs& a, hipStream_t stream) {
         a.topk_ids, a.topk_weights, tables, act);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
-    const auto down = [&](auto tiles) {
+    const auto down = [&](auto tiles, auto pairs) {
         constexpr int RT = decltype(tiles)::value;
-        decode_down_kernel<W, RT><<<a.H / (4 * RT), kThreads, 0, stream>>>(
+        decode_down_kernel<W, RT, decltype(pairs)::value><<<a.H / (4 * RT), kThreads, 0, stream>>>(
             a.T, a.k, static_cast<const uint8_t*>(a.w_down), a.s_down, a.H, a.I, tables, act, a.topk_weights,
             static_cast<uint16_t*>(a.out));
         return hipGetLastError();
     };
     if constexpr (std::is_same_v<W, Bf16Weights>)
-        return down(std::integral_constant<int, 1>{});
+        return down(std::integral_constant<int, 1>{}, std::false_type{});
     else if (a.H >= kWideDown)
-        return down(std::integral_constant<int, 4>{});
+        return down(std::integral_constant<int, 4>{}, std::false_type{});
     else
-        return down(std::integral_constant<int, 1>{});
+        return down(std::integral_constant<int, 1>{}, std::true_type{});
 }
 
 template <class W>

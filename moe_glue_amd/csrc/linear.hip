@@ -31,7 +31,7 @@ __global__ __launch_bounds__(kThreads, NT == 1 ? 4 : 2) void linear_mxfp4_kernel
     const int c0 = (int)blockIdx.y * (4 * NT);
     const uint32_t row_bytes = W::bytes_of((uint32_t)K), row_scales = W::row_scales(K);
     RowTiles<kTiles> rows;
-    uint32_t col[NT];
+    uint32_t col[1][NT];
     f32x4 acc[kTiles][NT];
 #pragma unroll
     for (int r = 0; r < kTiles; ++r) {
@@ -45,11 +45,11 @@ __global__ __launch_bounds__(kThreads, NT == 1 ? 4 : 2) void linear_mxfp4_kernel
 #pragma unroll
     for (int c = 0; c < NT; ++c) {
         const int t = c0 + c * 4 + lane % 16 / 4;
-        col[c] = t < T ? (uint32_t)t * (uint32_t)K * 2 : kNowhere;
+        col[0][c] = t < T ? (uint32_t)t * (uint32_t)K * 2 : kNowhere;
     }
     const int steps = steps_of<W>(K);
     const __amdgpu_buffer_rsrc_t wb = buffer_of(w + (size_t)n0 * row_bytes, (size_t)(N - n0) * row_bytes);
-    multiply_rows<W, kTiles, NT, (NT == 2 ? 4 : 2), kCacheNt>(wb, wb, rows, buffer_of(x, (size_t)T * K * 2), col, K,
+    multiply_rows<W, kTiles, NT, (NT == 2 ? 4 : 2), kCacheNt, 1>(wb, wb, rows, buffer_of(x, (size_t)T * K * 2), col, K,
                                                               steps * wave / kWaves,
                                                               steps * (wave + 1) / kWaves, acc);
 #pragma unroll

@@ -165,28 +165,32 @@ struct RowTiles {
 // The loads of U steps are in flight: a step's registers are loaded again, for
 // the step U later, as soon as it is multiplied.  In a step that K ends inside,
 // lanes past K hold zeros.  CACHE: the weight loads' cache bits, kCacheNt where
-// no other wave will read them.
-template <class W, int RT, int NT, int U, int CACHE>
+// no other wave will read them.  CT = 2: odd row tiles have columns of their own,
+// col[1] (two products side by side, for the loads in flight); CT = 1: all share
+// col[0].
+template <class W, int RT, int NT, int U, int CACHE, int CT>
 __device__ __forceinline__ void multiply_rows(__amdgpu_buffer_rsrc_t w0, __amdgpu_buffer_rsrc_t w1,
                                               const RowTiles<RT>& rows, __amdgpu_buffer_rsrc_t x,
-                                              const uint32_t (&col)[NT], int K, int s0, int s1,
+                                              const uint32_t (&col)[CT][NT], int K, int s0, int s1,
                                               f32x4 (&acc)[RT][NT]) {
     constexpr int PIECE = W::STEP / 16;
     static_assert(PIECE == 8 * W::SUB, "a lane's piece is its MFMAs' k");
     const uint32_t lane = threadIdx.x % kWave;
     const uint32_t piece = (lane / 16 * 4 + lane % 4) * PIECE;
     const uint32_t row = lane % 16 / 4;
-    uint32_t a_at[RT], sc_row[RT], b_at[NT];
+    uint32_t a_at[RT], sc_row[RT], b_at[CT][NT];
 #pragma unroll
     for (int r = 0; r < RT; ++r) {
         a_at[r] = min(row, rows.last[r]) * W::bytes_of((uint32_t)K) + W::bytes_of(piece);
         sc_row[r] = min(row, rows.last[r]) * W::row_scales(K);
     }
 #pragma unroll
-    for (int c = 0; c < NT; ++c) b_at[c] = col[c] < kNowhere ? col[c] + piece * 2 : kNowhere;
+    for (int g = 0; g < CT; ++g)
+#pragma unroll
+        for (int c = 0; c < NT; ++c) b_at[g][c] = col[g][c] < kNowhere ? col[g][c] + piece * 2 : kNowhere;
     typename W::Frag a[U][RT];
     typename W::Scales sc[RT];
-    u32x4 b[U][NT][W::SUB];
+    u32x4 b[U][CT][NT][W::SUB];
     const int partial = K / W::STEP;  // the step that K ends inside, if it does
     const auto load = [&](auto index, int s, bool whole) {
         constexpr int u = decltype(index)::value;
@@ -197,12 +201,14 @@ __device__ __forceinline__ void multiply_rows(__amdgpu_buffer_rsrc_t w0, __amdgp
             a[u][r] = W::template load<CACHE>(r % 2 == 0 ? w0 : w1, past ? kNowhere : a_at[r],
                                               rows.at[r] + W::bytes_of(k));
 #pragma unroll
-        for (int c = 0; c < NT; ++c)
+        for (int g = 0; g < CT; ++g)
 #pragma unroll
-            for (int m = 0; m < W::SUB; ++m)
-                b[u][c][m] = __builtin_bit_cast(
-                    u32x4, __builtin_amdgcn_raw_buffer_load_b128(x, (int)((past ? kNowhere : b_at[c]) + m * 16),
-                                                                 (int)(k * 2), 0));
+            for (int c = 0; c < NT; ++c)
+#pragma unroll
+                for (int m = 0; m < W::SUB; ++m)
+                    b[u][g][c][m] = __builtin_bit_cast(
+                        u32x4, __builtin_amdgcn_raw_buffer_load_b128(
+                                   x, (int)((past ? kNowhere : b_at[g][c]) + m * 16), (int)(k * 2), 0));
     };
     const auto scales_at = [&](int s) {  // at a group's first step
         if constexpr (W::SCALE_STEPS > 0)
@@ -227,7 +233,7 @@ __device__ __forceinline__ void multiply_rows(__amdgpu_buffer_rsrc_t w0, __amdgp
 #pragma unroll
                 for (int c = 0; c < NT; ++c)
                     acc[r][c] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
-                        av, __builtin_bit_cast(bf16x8, b[u][c][m]), acc[r][c], 0, 0, 0);
+                        av, __builtin_bit_cast(bf16x8, b[u][r % CT][c][m]), acc[r][c], 0, 0, 0);
             }
         });
     };
