@@ -321,16 +321,15 @@ moe_status moe_combine(const uint16_t* y, const float* topk_weights, const int32
 #define MOE_NORM_H_MAX 65536 /* widest normalised row                               */
 
 /* Root-mean-square norm of the residual stream, before the router and the
- * experts.  For each row t, in fp32:
+ * experts.  For each row t, in fp32 (the row sum and the root in fp64):
  *   s = x[t, :] + residual[t, :]          (residual may be NULL: s = x[t, :])
  *   n = s / sqrt(mean(s^2) + eps) * weight
  *   residual_out[t, :] = bf16(s)          (NULL: not written)
  *   out[t, :] = bf16(n)
  * Each result is rounded once, to nearest even: n is formed from the unrounded
- * s.  The row sum is formed in fp32, in an order that depends on H alone; rows
- * whose squares pass fp32's range are scaled first.  A row with an infinity or
- * a NaN normalises as the formula does (NaN at the infinities and 0 beside
- * them; a NaN makes the whole row NaN).
+ * s.  A row's result depends on H and the row alone, not on its batch.  A row with
+ * an infinity or a NaN normalises as the formula does (NaN at the infinities and
+ * 0 beside them; a NaN makes the whole row NaN).
  * x, residual, residual_out, out bf16 [T, H]; weight bf16 [H].  H % 8 == 0,
  * H <= MOE_NORM_H_MAX; every pointer 16-byte aligned.  eps must be finite and
  * a positive normal fp32.  residual_out may be the very buffer residual (the
@@ -356,7 +355,8 @@ moe_status moe_rmsnorm_fp8(const uint16_t* x, const uint16_t* residual, const ui
 
 /* moe_rmsnorm with MXFP8 output: n (fp32) quantised per 32 consecutive columns
  * in the format of moe_expand_rows_mxfp8 (E8M0 scale byte e + 127,
- * e = max(floor(log2 amax) - 8, -127), codes E4M3(clamp(n / 2^e, +-448))).  A
+ * e = max(floor(log2 amax) - 8, -127) of the unrounded maximum, codes
+ * E4M3(clamp(n / 2^e, +-448))).  A
  * block with a NaN or an infinity in n has the scale byte 255 (NaN) and codes
  * 0x7F.  codes uint8 [T, H]; scales uint8 [T, H/32]; H % 32 == 0; otherwise as
  * moe_rmsnorm_fp8. */

@@ -6,13 +6,18 @@
 //   out = bf16(n), or E4M3 codes of n with fp32 or E8M0 block scales
 //
 // Bound by HBM: about 6 operations for 6 to 8 bytes (8192 x 7168 with residual
-// and MXFP8 out moves 412 MB in 68 us, 6.0 TB/s).  A row stays in
+// and MXFP8 out moves 412 MB in 70 us, 5.9 TB/s).  A row stays in
 // registers from its load to its store, so x and r are read once.  One
 // workgroup takes one row with WPR waves of NV 16-byte vectors a lane; the
 // sum of squares crosses lanes by DPP and waves by LDS, in an order that
 // depends on H alone, so a row's result does not depend on its batch.
-// n is rounded once, straight from fp32, in every format (codes are not
-// taken of a bf16 row).
+// The sum of squares and the root are formed in fp64, which has the range for
+// any fp32 square; n is then right to two fp32 steps.  An MXFP8 scale is a power
+// of two, decided by which power the block's maximum reaches, so a maximum that
+// near to one is looked at with the products' rounding errors: decided in fp32
+// about one block in six million took the neighbouring scale.  (All products in
+// fp64: 72.4 us instead of 70.0 at 8192 x 7168.)  n is rounded once in every format: codes are not taken
+// of a bf16 row.
 #include "fp8_common.h"
 #include "kernels.h"
 
@@ -22,14 +27,38 @@ namespace {
 enum NormMode { kNormBf16 = 0, kNormFp8 = 1, kNormMx = 2 };
 
 constexpr uint32_t kInfBits = 0x7F800000u;
+// fp32 steps that n may be off by: two products and the factor's own rounding,
+// half a step each, with room to spare.
+constexpr uint32_t kNear = 8;
+
+// Sum over the 64 lanes of a wave, in every lane.
+template <int CTRL>
+__device__ __forceinline__ double add_dpp(double v) {
+    const u32x2 w = __builtin_bit_cast(u32x2, v);
+    return v + __builtin_bit_cast(double, u32x2{dpp<CTRL>(w[0]), dpp<CTRL>(w[1])});
+}
+__device__ __forceinline__ double wave_sum(double v) {
+    v = add_dpp<kQuadXor1>(v);
+    v = add_dpp<kQuadXor2>(v);
+    v = add_dpp<kRowHalfMirror>(v);
+    v = add_dpp<kRowMirror>(v);
+    u32x2 w = __builtin_bit_cast(u32x2, v);
+    auto lo = __builtin_amdgcn_permlane16_swap(w[0], w[0], false, false);
+    auto hi = __builtin_amdgcn_permlane16_swap(w[1], w[1], false, false);
+    v = __builtin_bit_cast(double, u32x2{lo[0], hi[0]}) + __builtin_bit_cast(double, u32x2{lo[1], hi[1]});
+    w = __builtin_bit_cast(u32x2, v);
+    lo = __builtin_amdgcn_permlane32_swap(w[0], w[0], false, false);
+    hi = __builtin_amdgcn_permlane32_swap(w[1], w[1], false, false);
+    return __builtin_bit_cast(double, u32x2{lo[0], hi[0]}) + __builtin_bit_cast(double, u32x2{lo[1], hi[1]});
+}
 
 template <int WPR>
-__device__ __forceinline__ float row_sum(float v, float* s_part) {
-    v = __builtin_bit_cast(float, group_reduce<kWave, Op::FAdd>(__builtin_bit_cast(uint32_t, v)));
+__device__ __forceinline__ double row_sum(double v, double* s_part) {
+    v = wave_sum(v);
     if constexpr (WPR > 1) {
         if (threadIdx.x % kWave == 0) s_part[threadIdx.x / kWave] = v;
         __syncthreads();
-        v = 0.0f;
+        v = 0.0;
 #pragma unroll
         for (int w = 0; w < WPR; ++w) v += s_part[w];
     }
@@ -38,12 +67,12 @@ __device__ __forceinline__ float row_sum(float v, float* s_part) {
 
 template <int WPR, int NV, int MODE>
 __global__ __launch_bounds__(kWave* WPR) void rmsnorm_kernel(const u32x4* __restrict__ x, const u32x4* r,
-                                                             const u32x4* __restrict__ w, uint32_t n8, float width,
+                                                             const u32x4* __restrict__ w, uint32_t n8, double width,
                                                              float eps, u32x4* r_out, u32x4* out,
                                                              u32x2* __restrict__ codes, void* __restrict__ scales,
                                                              int gl) {
     constexpr int THREADS = kWave * WPR;
-    __shared__ float s_part[2][WPR];
+    __shared__ double s_part[WPR];
     const size_t base = (size_t)blockIdx.x * n8;
     u32x4 xv[NV], rv[NV], wv[NV];
 #pragma unroll
@@ -66,7 +95,7 @@ __global__ __launch_bounds__(kWave* WPR) void rmsnorm_kernel(const u32x4* __rest
         if (c < n8) wv[i] = w[c];
     }
     float s[NV][8];
-    float sq = 0.0f;
+    double sq = 0.0;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
         unpack8(xv[i], s[i]);
@@ -77,7 +106,7 @@ __global__ __launch_bounds__(kWave* WPR) void rmsnorm_kernel(const u32x4* __rest
             for (int e = 0; e < 8; ++e) s[i][e] += f[e];
         }
 #pragma unroll
-        for (int e = 0; e < 8; ++e) sq = fmaf(s[i][e], s[i][e], sq);
+        for (int e = 0; e < 8; ++e) sq = fma((double)s[i][e], (double)s[i][e], sq);
     }
     if (r_out != nullptr)
 #pragma unroll
@@ -85,35 +114,46 @@ __global__ __launch_bounds__(kWave* WPR) void rmsnorm_kernel(const u32x4* __rest
             const uint32_t c = threadIdx.x + i * THREADS;
             if (c < n8) store_stream(r_out + base + c, pack8(s[i]));
         }
-    float sum = row_sum<WPR>(sq, s_part[0]);
-    if (!(sum < __builtin_inff())) {
-        // squares beyond fp32 (|s| from 2^64): once more on s * 2^-80, whose
-        // squares cannot overflow (an infinite or NaN s still does: NaN)
-        sq = 0.0f;
-        eps *= 0x1p-80f * 0x1p-80f;
-#pragma unroll
-        for (int i = 0; i < NV; ++i)
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                s[i][e] *= 0x1p-80f;
-                sq = fmaf(s[i][e], s[i][e], sq);
-            }
-        sum = row_sum<WPR>(sq, s_part[1]);
-    }
-    const float rstd = 1.0f / sqrtf(sum / width + eps);
+    const double rstd = 1.0 / sqrt(row_sum<WPR>(sq, s_part) / width + (double)eps);
+    // where fp32 would hold 1 / rms as a subnormal, both factors move by 2^80
+    const bool huge = rstd < 0x1p-100;
+    const float pre = huge ? 0x1p-80f : 1.0f;
+    const float scaled = (float)(huge ? rstd * 0x1p80 : rstd);
+    const float scaled_low = (float)((huge ? rstd * 0x1p80 : rstd) - (double)scaled);
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
         const uint32_t c = threadIdx.x + i * THREADS;
         float f[8], n[8];
         unpack8(wv[i], f);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) n[e] = s[i][e] * rstd * f[e];
+        for (int e = 0; e < 8; ++e) n[e] = s[i][e] * pre * scaled * f[e];
         if (out != nullptr && c < n8) store_stream(out + base + c, pack8(n));
         if constexpr (MODE != kNormBf16) {
             // a scale group is gl consecutive lanes; H is a multiple of it, so
             // a group lies whole inside or whole past the row
             const uint32_t amax = group_abs_max(abs_max_bits8(n), gl);
             BlockScale b = block_scale(amax, MODE == kNormMx);
+            if constexpr (MODE == kNormMx) {
+                // a maximum within fp32's error of a power of two: whether it reaches
+                // it decides the scale, so look again with the products' low parts
+                // (fma gives a product's rounding error exactly)
+                const bool near = (amax + kNear) % 0x800000u < 2 * kNear && amax < kInfBits;
+                if (__any(near)) {
+                    // short of it by less than the low parts' own error, 2^-44 of
+                    // it, is on it: rows of one magnitude land there
+                    const uint32_t edge = (amax + kNear) & 0xFF800000u;
+                    const float at = __builtin_bit_cast(float, edge), slack = at * 0x1p-44f;
+                    uint32_t reaches = 0;
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        const float v = s[i][e] * pre, p = v * f[e], h = p * scaled;
+                        const float low = fmaf(p, scaled_low, fmaf(fmaf(v, f[e], -p), scaled, fmaf(p, scaled, -h)));
+                        if (fabsf(h) - at + (h < 0.0f ? -low : low) >= -slack) reaches = 1;
+                    }
+                    reaches = group_abs_max(reaches, gl);
+                    if (near) b = block_scale(reaches ? edge : edge - 1, true);
+                }
+            }
             u32x2 q = quantize8_e4m3(n, b.inv, b.pre);
             if (amax >= kInfBits) {  // a NaN or an infinity in the group: NaN scale, NaN codes
                 b.scale = __builtin_nanf("");
@@ -135,7 +175,7 @@ hipError_t launch_shape(const NormArgs& a, hipStream_t stream) {
     const auto go = [&](auto kernel) {
         kernel<<<a.T, kWave * WPR, 0, stream>>>(
             static_cast<const u32x4*>(a.x), static_cast<const u32x4*>(a.residual),
-            static_cast<const u32x4*>(a.weight), n8, (float)a.H, a.eps, static_cast<u32x4*>(a.residual_out),
+            static_cast<const u32x4*>(a.weight), n8, (double)a.H, a.eps, static_cast<u32x4*>(a.residual_out),
             static_cast<u32x4*>(a.out), static_cast<u32x2*>(a.codes), a.scales, a.group / 8);
         return hipGetLastError();
     };

@@ -169,6 +169,28 @@ def test_rmsnorm_codes_bit_exact_where_n_is_a_bf16(dev, oracle_lib, fmt):
     compare.assert_equal(scales.cpu().numpy(), sr, "scales")
 
 
+@pytest.mark.parametrize("H", [32, 2048, 7168])
+def test_rmsnorm_mxfp8_scale_of_a_maximum_just_below_a_power_of_two(dev, H):
+    """Rows of +-15/8 normalise to +-1 / sqrt(1 + eps / R), R = 225/64: with eps =
+    7e-8 that is 1 - 1e-8, which fp32 would round to 1.  Its scale is still that
+    of a maximum below 1 (2^-9, codes saturated); without eps to speak of n is 1
+    (2^-8, code 256)."""
+    import torch
+    import moe_glue_amd as mg
+
+    rng = np.random.default_rng(H)
+    T = 4
+    sign = rng.choice([-1.0, 1.0], (T, H))
+    x = G.to_dev(inputs.f32_to_bf16_bits((1.875 * sign).astype(np.float32)), dev)
+    shift = rng.integers(-3, 4, H // 32)  # blocks of w = 2^j
+    w = G.to_dev(inputs.f32_to_bf16_bits(np.repeat(2.0 ** shift, 32).astype(np.float32)), dev)
+    for eps, exponent, code in ((7e-8, -9, 0x7E), (2e-38, -8, 0x78)):
+        codes, scales, _ = mg.rmsnorm_mxfp8(x, w, eps=eps)
+        torch.cuda.synchronize()
+        compare.assert_equal(scales.cpu().numpy().astype(int), np.tile(127 + exponent + shift, (T, 1)), f"eps {eps}")
+        compare.assert_equal(codes.cpu().numpy(), np.where(sign < 0, code | 0x80, code).astype(np.uint8), f"eps {eps}")
+
+
 def test_rmsnorm_row_does_not_depend_on_its_batch(dev):
     import torch
     import moe_glue_amd as mg
