@@ -10,19 +10,25 @@
 // round loads in flight, with the products on the matrix cores (mfma_rows.h).
 //
 // Launch 1.  No workgroup waits for another, so each recomputes the routing in
-// LDS (as the one-launch dispatch does) and then walks its share of the items
-// (expert, 16 gate rows and their 16 up rows).  The eight waves of a workgroup
-// split K, so even one token's few experts keep the whole chip loading; their
-// partial sums meet in LDS, where gate and up of one output lie side by side
-// for the SwiGLU.  act is rounded to bf16 there, the operand type of the second
-// product.  Workgroup 0 writes the ids, the weights and the tables that launch
-// 2 reads.
+// LDS (as the one-launch dispatch does; about 4 us) and then walks its share of
+// the row quads: 4 gate rows and their 4 up rows of an expert, whose products with
+// one token a lane holds together for the SwiGLU.  In whole rounds of the grid a
+// wave has all of K to itself, and no barrier; what is left over, all there is
+// with one token, is split along K between the waves and meets in LDS.  act is
+// rounded to bf16, the operand type of the second product.  Workgroup 0 writes the
+// ids, the weights and the tables that launch 2 reads.
 //
-// Launch 2.  A workgroup owns a few output columns (4 rows of w_down, 8 with
-// MXFP4) for every token, so the sum over experts needs no atomics and no third
-// launch.  Its waves deal the entries, and split K when there are few.
-// fp32 y meets in LDS and is summed over j in order, so the same call always
-// gives the same bits.
+// Launch 2.  A workgroup owns a few output columns for every token, so the sum
+// over experts needs no atomics and no third launch.  Its waves deal the entries,
+// and split K when there are few.  fp32 y meets in LDS and is summed over j in
+// order, so the same call always gives the same bits.
+//
+// Measured (us, launch 1 + launch 2; the weights read at the rate of a large
+// streaming read, 6.7 TB/s, in brackets): one token, 128 experts of 2048 x 768,
+// bf16, 12.1 + 6.8 (11.3 together); 32 tokens 116 + 58 (155); 8 tokens, some 42 of
+// 64 experts of 7168 x 2048, bf16, 347 + 169 (550); 16 tokens, 256 experts of 7168 x
+// 2048, MXFP4, 228 + 128 (285); 61 tokens, skewed, 64 experts of 4096 x 1408,
+// MXFP4, 86 + 51 (47; here the columns' loads and the products count too).
 #include "kernels.h"
 #include "mfma_rows.h"
 #include "route_common.h"
