@@ -131,10 +131,8 @@ __global__ __launch_bounds__(kThreads) void linear_mxfp4_wide_kernel(const uint1
         x_at[c] = (uint32_t)min(c * 16 + tid / 32, T - 1) * (uint32_t)K * 2 + (uint32_t)x_piece * 16;
     u32x4 wv[kAhead], xv[kAhead][NT];
     uint8_t sv[kAhead];
-    const int turn = (int)(blockIdx.x % (uint32_t)chunks);
     const auto fetch = [&](auto index, int chunk) {
         constexpr int j = decltype(index)::value;
-        chunk = chunk + turn < chunks ? chunk + turn : chunk + turn - chunks;
         // past K: zeros (codes of zero under scale byte 0)
         const bool in_w = chunk * kChunk + w_piece * 32 < K, in_x = chunk * kChunk + x_piece * 8 < K;
         wv[j] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(

@@ -220,6 +220,26 @@ def test_norm_and_linear_and_layer_take_empty_batches(dev):
     torch.cuda.synchronize()
 
 
+@pytest.mark.parametrize("fmt", ["bf16", "fp8", "mxfp8"])
+@pytest.mark.parametrize("T,H", [((1 << 22) + 5, 32), (70001, 32768)])
+def test_rmsnorm_many_rows(dev, fmt, T, H):
+    """More rows than one launch takes, and tensors past 2^32 bytes: the last rows
+    are what they are alone."""
+    import torch
+    import moe_glue_amd as mg
+
+    _log(f"[norm many] {fmt} {T}x{H}")
+    x = torch.empty((T, H), dtype=torch.bfloat16, device=dev).normal_(generator=torch.Generator(dev).manual_seed(3))
+    w = torch.ones(H, dtype=torch.bfloat16, device=dev) * 1.5
+    call = {"bf16": lambda v: mg.rmsnorm(v, w)[:1], "fp8": lambda v: mg.rmsnorm_fp8(v, w, 32)[:2],
+            "mxfp8": lambda v: mg.rmsnorm_mxfp8(v, w)[:2]}[fmt]
+    whole = call(x)
+    for lo, hi in ((0, 3), ((1 << 21) - 1, (1 << 21) + 2), (T - 7, T)):
+        if hi <= T:
+            for a, b in zip(whole, call(x[lo:hi].contiguous())):
+                assert torch.equal(a[lo:hi].view(torch.uint8), b.view(torch.uint8)), (lo, hi)
+
+
 # ------------------------------------------------------------------ MXFP4
 def mxfp4(rng, shape, lo=118, hi=122):
     *lead, K = shape
@@ -343,6 +363,37 @@ def test_decode_layer(dev, fmt, shape, kind):
     torch.cuda.synchronize()
     for key in ("topk_ids", "topk_weights", "out"):
         assert np.array_equal(first[key], raws[key].cpu().numpy()), f"{key} changed on the second call"
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "mxfp4"])
+def test_decode_layer_of_experts_past_32_bits(dev, fmt):
+    """Weights of more than 2^32 bytes (and 2^32 values): the last experts give
+    what they give in a tensor of their own."""
+    import torch
+    import moe_glue_amd as mg
+
+    E, few, k, H, I = 160, 4, 2, 8192, 2048
+    _log(f"[layer big] {fmt} E={E} H={H} I={I}")
+    rng = np.random.default_rng(9)
+    T = 5
+    x = G.to_dev(bf16(rng, (T, H)), dev)
+    small_logits = rng.standard_normal((T, few)).astype(np.float32)
+    logits = np.full((T, E), -50.0, np.float32)
+    logits[:, E - few:] = small_logits
+    if fmt == "bf16":
+        last = [G.to_dev(bf16(rng, s, 0.02), dev) for s in ((few, 2 * I, H), (few, H, I))]
+    else:
+        last = [G.to_dev(v, dev) for s in ((few, 2 * I, H), (few, H, I)) for v in mxfp4(rng, s)]
+    big = []
+    for v in last:
+        t = torch.zeros((E, *v.shape[1:]), dtype=v.dtype, device=dev)
+        t[E - few:] = v
+        big.append(t)
+    a = run_layer(mg, k, G.to_dev(logits, dev), None, x, big)
+    b = run_layer(mg, k, G.to_dev(small_logits, dev), None, x, last)
+    torch.cuda.synchronize()
+    assert torch.equal(a["topk_ids"], b["topk_ids"] + (E - few))
+    assert torch.equal(a["out"].view(torch.int16), b["out"].view(torch.int16))
 
 
 @pytest.mark.parametrize("T", [1, 9, 64])
