@@ -77,10 +77,12 @@ __global__ __launch_bounds__(kThreads, NT == 1 ? 4 : 2) void linear_mxfp4_kernel
 // read from LDS once per 16 R x 16 NT products.  Chunks are fetched kAhead ahead
 // into registers and pass through two LDS buffers with one barrier each.  Rows
 // of LDS are padded by 16 bytes: the 16 rows a fragment read touches then fall
-// into different banks.  At 64 tokens and 7168 x 16384 a chunk takes 0.87 us of
-// which, left out one at a time, the loads account for 0.2, the writes to LDS
-// for 0.33 and the rest (LDS reads, products) for 0.38: they add up, hardly
-// overlapping behind the one barrier.
+// into different banks.  A chunk's LDS writes, loads, LDS reads and products go
+// by turns, a fourth of each at a time: all of one kind and then all of the next
+// queue up behind each other (64 tokens, 7168 x 16384: 31.0 us, by turns 27.7;
+// without any loads 21, so LDS and products are most of it).  Waves with chunks
+// and LDS of their own, without barriers, measured 10 to 15 % less below 8192
+// rows of W and 25 % more above, where their shorter pieces of a row cost HBM.
 constexpr int kChunk = 256;
 // chunks in flight, by registers
 template <int NT>
@@ -131,18 +133,25 @@ __global__ __launch_bounds__(kThreads) void linear_mxfp4_wide_kernel(const uint1
         x_at[c] = (uint32_t)min(c * 16 + tid / 32, T - 1) * (uint32_t)K * 2 + (uint32_t)x_piece * 16;
     u32x4 wv[kAhead], xv[kAhead][NT];
     uint8_t sv[kAhead];
-    const auto fetch = [&](auto index, int chunk) {
+    const auto fetch_w = [&](auto index, int chunk) {
         constexpr int j = decltype(index)::value;
         // past K: zeros (codes of zero under scale byte 0)
-        const bool in_w = chunk * kChunk + w_piece * 32 < K, in_x = chunk * kChunk + x_piece * 8 < K;
+        const bool in_w = chunk * kChunk + w_piece * 32 < K;
         wv[j] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(
                                               wb, (int)(in_w ? w_at : kNowhere), chunk * (kChunk / 2), kCacheNt));
         sv[j] = (uint8_t)__builtin_amdgcn_raw_buffer_load_b8(sb, (int)(in_w ? s_at : kNowhere),
                                                              chunk * (kChunk / 32), 0);
+    };
+    const auto fetch_x = [&](auto index, int chunk, int c) {
+        constexpr int j = decltype(index)::value;
+        const bool in_x = chunk * kChunk + x_piece * 8 < K;
+        xv[j][c] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(
+                                                 xb, (int)(in_x ? x_at[c] : kNowhere), chunk * (kChunk * 2), 0));
+    };
+    const auto fetch = [&](auto index, int chunk) {
+        fetch_w(index, chunk);
 #pragma unroll
-        for (int c = 0; c < NT; ++c)
-            xv[j][c] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(
-                                                     xb, (int)(in_x ? x_at[c] : kNowhere), chunk * (kChunk * 2), 0));
+        for (int c = 0; c < NT; ++c) fetch_x(index, chunk, c);
     };
     f32x4 acc[R][NT];
 #pragma unroll
@@ -150,47 +159,64 @@ __global__ __launch_bounds__(kThreads) void linear_mxfp4_wide_kernel(const uint1
 #pragma unroll
         for (int c = 0; c < NT; ++c) acc[r][c] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 
-    const auto to_lds = [&](auto index, int buf) {
+    const auto to_lds_w = [&](auto index, int buf) {
         constexpr int j = decltype(index)::value;
         if (has_w) {
             *reinterpret_cast<u32x4*>(&sh.w[buf][w_row][w_piece * 16]) = wv[j];
             sh.sc[buf][w_row][w_piece] = sv[j];
         }
+    };
+    const auto to_lds_x = [&](auto index, int buf, int c) {
+        constexpr int j = decltype(index)::value;
+        *reinterpret_cast<u32x4*>(&sh.x[buf][c * 16 + tid / 32][x_piece * 16]) = xv[j][c];
+    };
+    const auto to_lds = [&](auto index, int buf) {
+        to_lds_w(index, buf);
 #pragma unroll
-        for (int c = 0; c < NT; ++c)
-            *reinterpret_cast<u32x4*>(&sh.x[buf][c * 16 + tid / 32][x_piece * 16]) = xv[j][c];
+        for (int c = 0; c < NT; ++c) to_lds_x(index, buf, c);
     };
     // this wave's operands of a chunk, out of LDS a chunk ahead of their use
     uint32_t codes[2][R], scale[2][R];
     u32x4 b[2][NT];
+    const auto from_lds_w = [&](int buf, int r) {
+        const int row = r * 16 + lane % 16;
+        codes[buf][r] = *reinterpret_cast<const uint32_t*>(&sh.w[buf][row][wave * 16 + lane / 16 * 4]);
+        scale[buf][r] = sh.sc[buf][row][wave];
+    };
+    const auto from_lds_x = [&](int buf, int c) {
+        b[buf][c] = *reinterpret_cast<const u32x4*>(&sh.x[buf][c * 16 + lane % 16][wave * 64 + lane / 16 * 16]);
+    };
     const auto from_lds = [&](int buf) {
 #pragma unroll
-        for (int r = 0; r < R; ++r) {
-            const int row = r * 16 + lane % 16;
-            codes[buf][r] = *reinterpret_cast<const uint32_t*>(&sh.w[buf][row][wave * 16 + lane / 16 * 4]);
-            scale[buf][r] = sh.sc[buf][row][wave];
-        }
+        for (int r = 0; r < R; ++r) from_lds_w(buf, r);
 #pragma unroll
-        for (int c = 0; c < NT; ++c)
-            b[buf][c] = *reinterpret_cast<const u32x4*>(&sh.x[buf][c * 16 + lane % 16][wave * 64 + lane / 16 * 16]);
+        for (int c = 0; c < NT; ++c) from_lds_x(buf, c);
     };
     // Chunk c: its operands are in registers, chunk c + 1 is in LDS (all waves
     // past the barrier have its pieces in, and have read chunk c out).  Chunk
     // c + 2 takes chunk c's buffer, and its registers chunk c + 2 + kAhead.
     const auto step = [&](auto index, int chunk) {
         constexpr int buf = decltype(index)::value % 2;
-        __syncthreads();
-        from_lds(1 - buf);
-        to_lds(index, buf);
-        fetch(index, min(chunk + 2 + kAhead, chunks - 1));
-#pragma unroll
-        for (int r = 0; r < R; ++r) {
+        const int next = min(chunk + 2 + kAhead, chunks - 1);
+        const auto products = [&](int r) {
             const bf16x8 a = Mxfp4Weights::values<0>(u32x2{codes[buf][r], 0u},
                                                      __builtin_bit_cast(float, scale[buf][r] << 23));
 #pragma unroll
             for (int c = 0; c < NT; ++c)
                 acc[r][c] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, __builtin_bit_cast(bf16x8, b[buf][c]),
                                                                     acc[r][c], 0, 0, 0);
+        };
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < (R > NT ? R : NT); ++i) {
+            if (i == 0) to_lds_w(index, buf);
+            if (i < NT) to_lds_x(index, buf, i);
+            if (i == 0) fetch_w(index, next);
+            if (i < NT) fetch_x(index, next, i);
+            if (i < R) from_lds_w(1 - buf, i);
+            if (i < NT) from_lds_x(1 - buf, i);
+            if (i < R) products(i);
+            __builtin_amdgcn_sched_barrier(0);  // (the compiler would gather them by kind)
         }
     };
     constexpr std::integral_constant<int, 0> first{};
@@ -257,12 +283,12 @@ hipError_t launch_nt(const void* x, int T, int K, const uint8_t* w, const uint8_
 
 hipError_t launch_linear_mxfp4(const void* x, int T, int K, const uint8_t* w, const uint8_t* scales, int N, void* y,
                                hipStream_t stream) {
-    // T = 1 to 64 tokens, the two kernels measured at K x N (us, rows kernel /
-    // staged one, T = 8, 16, 32, 64): 1024 x 1024 3.6 / 5.0, 4.5 / 5.0, 4.4 / 5.8,
-    // 4.5 / 7.3; 7168 x 4096 7.2 / 11.1, 9.8 / 11.8, 17.5 / 15.6, 33 / 21.6; 2048 x
-    // 7168 6.9 / 7.3, 9.0 / 7.4, 14.7 / 8.3, 24 / 11.0; 7168 x 16384 24 / 16.7, 34 /
-    // 17.9, 67 / 21.8, 130 / 31.8.
-    const int from = N <= 1024 ? MOE_DECODE_T_MAX : N <= 16 * kCus ? 16 : N <= 32 * kCus ? 8 : 4;
+    // The two kernels at K x N (us, rows kernel / staged one, T = 8, 16, 32, 64):
+    // 1024 x 1024 4.2 / 5.1, 4.9 / 4.6, 5.0 / 5.1, 5.0 / 6.6; 7168 x 2048 7.2 /
+    // 10.6, 9.9 / 11.3, 9.7 / 14.7, 16.7 / 20.7; 7168 x 4096 7.8 / 11.1, 10.2 / 11.9,
+    // 17.7 / 15.5, 34 / 21.6; 2048 x 7168 7.4 / 6.9, 9.5 / 7.0, 15.1 / 8.0, 25 / 11.1;
+    // 7168 x 16384 (T = 4: 15.8 / 18) 26 / 18.4, 36 / 19.6, 67 / 22.7, 129 / 27.7.
+    const int from = N <= 8 * kCus ? MOE_DECODE_T_MAX : N <= 16 * kCus ? 16 : N <= 32 * kCus ? 8 : 4;
     if (T > from) {
         const int rows = N <= 16 * kCus ? 1 : N <= 32 * kCus ? 2 : 4;  // one workgroup per CU as far as N reaches
         const auto nt = [&](auto r) {

@@ -269,7 +269,8 @@ def test_linear_mxfp4_every_code_and_scale(dev):
                                    (31, 2048, 70), (33, 1056, 31), (48, 992, 64), (64, 7168, 50), (64, 4096, 130),
                                    (1, 7168, 4096), (7, 16384, 19), (20, 96, 4097), (40, 1312, 5000), (9, 288, 4104),
                                    (5, 544, 8196), (33, 160, 8193), (64, 2016, 1030), (17, 256, 1028), (12, 32, 6001),
-                                   (64, 4128, 8200)])
+                                   (64, 4128, 8200), (17, 96, 2050), (33, 1056, 4095), (64, 160, 3001),
+                                   (13, 2336, 8195), (6, 2080, 8300)])
 def test_linear_mxfp4(dev, T, K, N):
     import torch
     import moe_glue_amd as mg
