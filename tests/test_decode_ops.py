@@ -397,6 +397,72 @@ def test_decode_layer_of_experts_past_32_bits(dev, fmt):
     assert torch.equal(a["out"].view(torch.int16), b["out"].view(torch.int16))
 
 
+@pytest.mark.parametrize("T,K,N", [(3, 96, 33), (8, 288, 70), (20, 96, 4100), (33, 544, 8197)])
+def test_linear_mxfp4_nan_stays_in_its_token_and_row(dev, T, K, N):
+    import torch
+    import moe_glue_amd as mg
+
+    _log(f"[linear nan] T={T} K={K} N={N}")
+    rng = np.random.default_rng(T)
+    x = bf16(rng, (T, K))
+    w, sc = mxfp4(rng, (N, K))
+    clean = G.to_host(mg.linear_mxfp4(*(G.to_dev(v, dev) for v in (x, w, sc))))
+    x[1, K - 1], x[2, 0] = 0x7FC0, 0x7F80  # NaN, infinity
+    sc[N - 1, K // 32 - 1] = 255
+    sc[5, 0] = 255
+    got = G.to_host(mg.linear_mxfp4(*(G.to_dev(v, dev) for v in (x, w, sc))))
+    rows = [n for n in range(N) if n not in (5, N - 1)]
+    tokens = [t for t in range(T) if t not in (1, 2)]
+    assert np.array_equal(got[tokens][:, rows], clean[tokens][:, rows])
+    isnan = (got & 0x7FFF) > 0x7F80
+    assert isnan[:, [5, N - 1]].all() and isnan[1].all()
+    assert ((got[2] & 0x7FFF) >= 0x7F80).all()
+    torch.cuda.synchronize()
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "mxfp4"])
+@pytest.mark.parametrize("T,H,I", [(1, 96, 32), (9, 96, 160), (40, 288, 96), (64, 4128, 64)])
+def test_decode_layer_nan_stays_in_its_token_and_expert(dev, fmt, T, H, I):
+    import torch
+    import moe_glue_amd as mg
+
+    _log(f"[layer nan] {fmt} T={T} H={H} I={I}")
+    E, k = 6, 2
+    rng = np.random.default_rng(T + H)
+    x = bf16(rng, (T, H))
+    logits = rng.standard_normal((T, E)).astype(np.float32)
+    if fmt == "bf16":
+        w = [bf16(rng, (E, 2 * I, H), 0.1), bf16(rng, (E, H, I), 0.1)]
+    else:
+        w = [v for s in ((E, 2 * I, H), (E, H, I)) for v in mxfp4(rng, s)]
+    on = lambda v: G.to_dev(v, dev)
+    ld, dev_w = on(logits), [on(v) for v in w]
+    clean = run_layer(mg, k, ld, None, on(x), dev_w)
+    ids, out = G.to_host(clean["topk_ids"]), G.to_host(clean["out"])
+    bad = ids[0, 0]
+    t = T - 1
+    poisoned = x.copy()
+    poisoned[t, H - 1] = 0x7FC0
+    got = G.to_host(run_layer(mg, k, ld, None, on(poisoned), dev_w)["out"])
+    assert np.array_equal(got[:t], out[:t]) and ((got[t] & 0x7FFF) > 0x7F80).all()
+
+    # one row of the expert's up weights: all outputs of its tokens; one row of its
+    # down weights: that output of them
+    routed = (ids == bad).any(axis=1)
+    for which, row, columns in ((0, 2 * I - 1, slice(None)), (1, H - 2, slice(H - 2, H - 1))):
+        v = [a.copy() for a in w]
+        if fmt == "bf16":
+            v[which][bad, row, -1] = 0x7FC0
+        else:
+            v[2 * which + 1][bad, row, -1] = 255
+        got = G.to_host(run_layer(mg, k, ld, None, on(x), [on(a) for a in v])["out"])
+        want = np.zeros(got.shape, bool)
+        want[routed, columns] = True
+        assert np.array_equal((got & 0x7FFF) > 0x7F80, want)
+        assert np.array_equal(got[~want], out[~want])
+    torch.cuda.synchronize()
+
+
 @pytest.mark.parametrize("T", [1, 9, 64])
 def test_layer_matches_the_separate_calls(dev, T):
     """The layer against the path's separate calls with library products between
