@@ -19,10 +19,9 @@ constexpr int kCus = 256;
 constexpr int kTiles = 4;  // row tiles of a workgroup: 16 rows of W
 
 template <int NT>
-__global__ __launch_bounds__(kThreads, NT == 1 ? 4 : 2) void linear_mxfp4_kernel(const uint16_t* __restrict__ x, int T, int K,
-                                                                const uint8_t* __restrict__ w,
-                                                                const uint8_t* __restrict__ sc, int N,
-                                                                uint16_t* __restrict__ y) {
+__global__ __launch_bounds__(kThreads, NT == 1 ? 4 : 2) void linear_mxfp4_kernel(
+    const uint16_t* __restrict__ x, int T, int K, const uint8_t* __restrict__ w, const uint8_t* __restrict__ sc, int N,
+    uint16_t* __restrict__ y) {
     using W = Mxfp4Weights;
     __shared__ float s_sums[kWaves][NT][kTiles][16];
     const int lane = (int)(threadIdx.x % kWave);
@@ -49,9 +48,8 @@ __global__ __launch_bounds__(kThreads, NT == 1 ? 4 : 2) void linear_mxfp4_kernel
     }
     const int steps = steps_of<W>(K);
     const __amdgpu_buffer_rsrc_t wb = buffer_of(w + (size_t)n0 * row_bytes, (size_t)(N - n0) * row_bytes);
-    multiply_rows<W, kTiles, NT, (NT == 2 ? 4 : 2), kCacheNt, 1>(wb, wb, rows, buffer_of(x, (size_t)T * K * 2), col, K,
-                                                              steps * wave / kWaves,
-                                                              steps * (wave + 1) / kWaves, acc);
+    multiply_rows<W, kTiles, NT, (NT == 2 ? 4 : 2), kCacheNt, 1>(
+        wb, wb, rows, buffer_of(x, (size_t)T * K * 2), col, K, steps * wave / kWaves, steps * (wave + 1) / kWaves, acc);
 #pragma unroll
     for (int c = 0; c < NT; ++c)
 #pragma unroll
@@ -206,7 +204,7 @@ __global__ __launch_bounds__(kThreads) void linear_mxfp4_wide_kernel(const uint1
                 acc[r][c] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, __builtin_bit_cast(bf16x8, b[buf][c]),
                                                                     acc[r][c], 0, 0, 0);
         };
-        __syncthreads();
+        __syncthreads();  // chunk + 1 is in LDS, and all have read this one out
 #pragma unroll
         for (int i = 0; i < (R > NT ? R : NT); ++i) {
             if (i == 0) to_lds_w(index, buf);
@@ -274,8 +272,8 @@ hipError_t launch_wide(const void* x, int T, int K, const uint8_t* w, const uint
 template <int NT>
 hipError_t launch_nt(const void* x, int T, int K, const uint8_t* w, const uint8_t* scales, int N, void* y,
                      hipStream_t stream) {
-    linear_mxfp4_kernel<NT><<<dim3((N + 15) / 16, (T + 4 * NT - 1) / (4 * NT)), kThreads, 0, stream>>>(static_cast<const uint16_t*>(x), T, K, w, scales,
-                                                                    N, static_cast<uint16_t*>(y));
+    linear_mxfp4_kernel<NT><<<dim3((N + 15) / 16, (T + 4 * NT - 1) / (4 * NT)), kThreads, 0, stream>>>(
+        static_cast<const uint16_t*>(x), T, K, w, scales, N, static_cast<uint16_t*>(y));
     return hipGetLastError();
 }
 

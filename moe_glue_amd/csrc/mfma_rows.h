@@ -51,8 +51,8 @@ __device__ __forceinline__ int wave_index() { return (int)uniform(threadIdx.x / 
 // That is all the range check is used for: every other offset plus its step lies
 // inside, whether or not the check counts the step.
 __device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer_of(const void* p, size_t bytes) {
-    return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), 0, (int)(uint32_t)(bytes < kNowhere ? bytes : kNowhere),
-                                             kRawBufferWord3);
+    return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), 0,
+                                             (int)(uint32_t)(bytes < kNowhere ? bytes : kNowhere), kRawBufferWord3);
 }
 
 // A lane's part of one row in a step (Frag), and what its tile's rows carry

@@ -179,7 +179,9 @@ hipError_t launch_shape(const NormArgs& a, hipStream_t stream) {
     const auto go = [&](auto kernel) {
         for (int row = 0; row < a.T; row += kMaxRows) {
             const size_t at = (size_t)row * n8;
-            const auto rows = [at](const void* p) { return p == nullptr ? nullptr : static_cast<const u32x4*>(p) + at; };
+            const auto rows = [at](const void* p) {
+                return p == nullptr ? nullptr : static_cast<const u32x4*>(p) + at;
+            };
             const auto out_rows = [at](void* p) { return p == nullptr ? nullptr : static_cast<u32x4*>(p) + at; };
             u32x2* codes = a.codes == nullptr ? nullptr : static_cast<u32x2*>(a.codes) + at;
             void* scales = a.codes == nullptr ? nullptr
