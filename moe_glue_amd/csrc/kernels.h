@@ -218,6 +218,20 @@ struct NormArgs {
     int group;           // columns per scale (32 with mx)
     bool mx;
 };
+// The rows of launch i of norm_launches(T).  A launch holds fewer than 2^32 lanes
+// (16 waves a row at most), so batches of more than kNormLaunchRows rows take
+// several; T may be any int32 >= 0, so the first row behind the last launch may
+// pass it.
+constexpr int64_t kNormLaunchRows = 1 << 21;
+struct NormLaunch {
+    int64_t first;
+    int32_t rows;
+};
+inline int norm_launches(int32_t T) { return (int)((T + kNormLaunchRows - 1) / kNormLaunchRows); }
+inline NormLaunch norm_launch(int32_t T, int i) {
+    const int64_t first = i * kNormLaunchRows, left = T - first;
+    return {first, (int32_t)(left < kNormLaunchRows ? left : kNormLaunchRows)};
+}
 hipError_t launch_rmsnorm(const NormArgs& a, hipStream_t stream);
 
 // ------------------------------------------------------- few-token products

@@ -169,16 +169,13 @@ __global__ __launch_bounds__(kWave* WPR) void rmsnorm_kernel(const u32x4* __rest
     }
 }
 
-// A launch holds fewer than 2^32 lanes: batches of more rows than this take
-// several.
-constexpr int kMaxRows = 1 << 21;
-
 template <int WPR, int NV>
 hipError_t launch_shape(const NormArgs& a, hipStream_t stream) {
     const uint32_t n8 = (uint32_t)a.H / 8;
     const auto go = [&](auto kernel) {
-        for (int row = 0; row < a.T; row += kMaxRows) {
-            const size_t at = (size_t)row * n8;
+        for (int i = 0; i < norm_launches(a.T); ++i) {
+            const NormLaunch part = norm_launch(a.T, i);
+            const size_t at = (size_t)part.first * n8;
             const auto rows = [at](const void* p) {
                 return p == nullptr ? nullptr : static_cast<const u32x4*>(p) + at;
             };
@@ -187,7 +184,7 @@ hipError_t launch_shape(const NormArgs& a, hipStream_t stream) {
             void* scales = a.codes == nullptr ? nullptr
                                               : static_cast<char*>(a.scales) +
                                                     at / (size_t)(a.group / 8) * (a.mx ? 1 : sizeof(float));
-            kernel<<<a.T - row < kMaxRows ? a.T - row : kMaxRows, kWave * WPR, 0, stream>>>(
+            kernel<<<part.rows, kWave * WPR, 0, stream>>>(
                 rows(a.x), rows(a.residual), static_cast<const u32x4*>(a.weight), n8, (double)a.H, a.eps,
                 out_rows(a.residual_out), out_rows(a.out), codes, scales, a.group / 8);
             const hipError_t e = hipGetLastError();
