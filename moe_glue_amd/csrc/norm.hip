@@ -136,8 +136,9 @@ __global__ __launch_bounds__(kWave* WPR) void rmsnorm_kernel(const u32x4* __rest
             if constexpr (MODE == kNormMx) {
                 // a maximum within fp32's error of a power of two: whether it reaches
                 // it decides the scale, so look again with the products' low parts
-                // (fma gives a product's rounding error exactly)
-                const bool near = (amax + kNear) % 0x800000u < 2 * kNear && amax < kInfBits;
+                // (fma gives a product's rounding error exactly).  A finite maximum
+                // below 2^128 does not reach it.
+                const bool near = (amax + kNear) % 0x800000u < 2 * kNear && amax + kNear < kInfBits;
                 if (__any(near)) {
                     // short of it by less than the low parts' own error, 2^-44 of
                     // it, is on it: rows of one magnitude land there

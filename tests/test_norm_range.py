@@ -3,6 +3,13 @@ leave fp32's range although the result does not."""
 import os
 import subprocess
 
+import numpy as np
+import pytest
+
+import compare
+import gpu_util as G
+from moe_glue_amd import inputs
+
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 
 
@@ -16,3 +23,39 @@ def test_launches_cover_every_batch_host(tmp_path):
                    check=True, capture_output=True)
     out = subprocess.run([str(exe)], capture_output=True, text=True, timeout=300)
     assert out.returncode == 0 and out.stdout.startswith("ok"), out.stdout + out.stderr
+
+
+@pytest.fixture(scope="module")
+def dev():
+    return G.device()
+
+
+def bits(a):
+    return inputs.f32_to_bf16_bits(np.asarray(a, np.float32))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("H", [64, 2048])
+@pytest.mark.parametrize("steps", [3, 4, 5, 6])
+def test_mxfp8_scale_of_a_maximum_just_below_2_128(dev, H, steps):
+    """Half of a row is +-2, half +-1, so rms^2 = 5/2 + eps, and w = 1.6 * 2^127: eps
+    puts the maximum `steps` fp32 steps below 2^128.  n is right to two steps, so
+    it is finite and its scale that of a maximum below 2^128: 2^(127 - 8), the
+    codes 448 (saturated) and 256 (255.99)."""
+    import torch
+    import moe_glue_amd as mg
+
+    print(f"[norm top] H={H} steps={steps}", flush=True)
+    rng = np.random.default_rng([H, steps])
+    T = 3
+    two = np.tile([2.0, 1.0], H // 2)
+    sign = rng.choice([-1.0, 1.0], (T, H))
+    w = bits(np.full(H, 1.6 * 2.0 ** 127))
+    w64 = float((w[:1].astype(np.uint32) << 16).view(np.float32)[0])
+    eps = (2 * (w64 * 2.0 ** -128) / (1 - steps * 2.0 ** -24)) ** 2 - 2.5
+    assert 1e-3 < eps < 1  # so that its own rounding moves n by less than a sixteenth of a step
+    codes, scales, _ = mg.rmsnorm_mxfp8(G.to_dev(bits(sign * two), dev), G.to_dev(w, dev), eps=eps)
+    torch.cuda.synchronize()
+    compare.assert_equal(scales.cpu().numpy(), np.full((T, H // 32), 246, np.uint8), "scales")
+    want = np.where(two == 2, 0x7E, 0x78) | np.where(sign < 0, 0x80, 0)
+    compare.assert_equal(codes.cpu().numpy(), want.astype(np.uint8), "codes")
