@@ -14,7 +14,7 @@
 // The sum of squares and the root are formed in fp64, which has the range for
 // any fp32 square; n is then right to two fp32 steps.  An MXFP8 scale is a power
 // of two, decided by which power the block's maximum reaches, so a maximum that
-// near to one is looked at with the products' rounding errors: decided in fp32
+// near to one is looked at again in fp64: decided in fp32
 // about one block in six million took the neighbouring scale.  (All products in
 // fp64: 72.4 us instead of 70.0 at 8192 x 7168.)  n is rounded once in every format: codes are not taken
 // of a bf16 row.
@@ -119,7 +119,6 @@ __global__ __launch_bounds__(kWave* WPR) void rmsnorm_kernel(const u32x4* __rest
     const bool huge = rstd < 0x1p-100;
     const float pre = huge ? 0x1p-80f : 1.0f;
     const float scaled = (float)(huge ? rstd * 0x1p80 : rstd);
-    const float scaled_low = (float)((huge ? rstd * 0x1p80 : rstd) - (double)scaled);
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
         const uint32_t c = threadIdx.x + i * THREADS;
@@ -135,22 +134,19 @@ __global__ __launch_bounds__(kWave* WPR) void rmsnorm_kernel(const u32x4* __rest
             BlockScale b = block_scale(amax, MODE == kNormMx);
             if constexpr (MODE == kNormMx) {
                 // a maximum within fp32's error of a power of two: whether it reaches
-                // it decides the scale, so look again with the products' low parts
-                // (fma gives a product's rounding error exactly).  A finite maximum
-                // below 2^128 does not reach it.
+                // it decides the scale, so look again with products in fp64, which
+                // neither pass its range nor fall below it.  A finite maximum below
+                // 2^128 does not reach it.
                 const bool near = (amax + kNear) % 0x800000u < 2 * kNear && amax + kNear < kInfBits;
                 if (__any(near)) {
-                    // short of it by less than the low parts' own error, 2^-44 of
-                    // it, is on it: rows of one magnitude land there
+                    // short of it by less than the row sum's and the products' own
+                    // errors, 2^-44 of it, is on it: rows of one magnitude land there
                     const uint32_t edge = (amax + kNear) & 0xFF800000u;
-                    const float at = __builtin_bit_cast(float, edge), slack = at * 0x1p-44f;
+                    const double reach = (double)__builtin_bit_cast(float, edge) * (1.0 - 0x1p-44);
                     uint32_t reaches = 0;
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        const float v = s[i][e] * pre, p = v * f[e], h = p * scaled;
-                        const float low = fmaf(p, scaled_low, fmaf(fmaf(v, f[e], -p), scaled, fmaf(p, scaled, -h)));
-                        if (fabsf(h) - at + (h < 0.0f ? -low : low) >= -slack) reaches = 1;
-                    }
+                    for (int e = 0; e < 8; ++e)
+                        if (fabs((double)s[i][e] * rstd * (double)f[e]) >= reach) reaches = 1;
                     reaches = group_abs_max(reaches, gl);
                     if (near) b = block_scale(reaches ? edge : edge - 1, true);
                 }

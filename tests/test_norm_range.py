@@ -59,3 +59,46 @@ def test_mxfp8_scale_of_a_maximum_just_below_2_128(dev, H, steps):
     compare.assert_equal(scales.cpu().numpy(), np.full((T, H // 32), 246, np.uint8), "scales")
     want = np.where(two == 2, 0x7E, 0x78) | np.where(sign < 0, 0x80, 0)
     compare.assert_equal(codes.cpu().numpy(), want.astype(np.uint8), "codes")
+
+
+@pytest.mark.gpu
+def test_mxfp8_scale_where_x_times_w_passes_fp32(dev):
+    """Rows of +-2^99 under w = 2^30 normalise to +-2^30 exactly, although the
+    products of x and w pass fp32's range: scale 2^(30 - 8), code 256."""
+    import torch
+    import moe_glue_amd as mg
+
+    rng = np.random.default_rng(0)
+    T, H = 4, 1024
+    sign = rng.choice([-1.0, 1.0], (T, H))
+    codes, scales, _ = mg.rmsnorm_mxfp8(G.to_dev(bits(sign * 2.0 ** 99), dev), G.to_dev(bits(np.full(H, 2.0 ** 30)), dev))
+    torch.cuda.synchronize()
+    compare.assert_equal(scales.cpu().numpy(), np.full((T, H // 32), 127 + 22, np.uint8), "scales")
+    compare.assert_equal(codes.cpu().numpy(), np.where(sign < 0, 0xF8, 0x78).astype(np.uint8), "codes")
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("below", [True, False])
+def test_mxfp8_scale_where_x_times_w_falls_below_fp32(dev, below):
+    """One block of four holds +-15/4 * 2^-40, so rms = 15/8 * 2^-40 (eps aside); the
+    others +-15/8 * 2^-105 under w = 2^-44: n = +-2^-109 times 1 / sqrt(1 + eps / rms^2),
+    and x w, 15/8 * 2^-149, is no fp32.  With eps = 7e-8 * 2^-80 n lies 1e-8 of it below
+    2^-109 and takes the scale 2^(-110 - 8), codes saturated; with the least eps,
+    2^-48 of it away, 2^(-109 - 8), code 256."""
+    import torch
+    import moe_glue_amd as mg
+
+    rng = np.random.default_rng(1)
+    T, H = 3, 512
+    sign = rng.choice([-1.0, 1.0], (T, H))
+    big = np.arange(H) // 32 % 4 == 1
+    x = sign * np.where(big, 3.75 * 2.0 ** -40, 1.875 * 2.0 ** -105)
+    w = np.where(big, 1.0, 2.0 ** -44)
+    eps = 7e-8 * 2.0 ** -80 if below else 1.2e-38
+    codes, scales, _ = mg.rmsnorm_mxfp8(G.to_dev(bits(x), dev), G.to_dev(bits(w), dev), eps=eps)
+    torch.cuda.synchronize()
+    small = scales.cpu().numpy()[:, np.arange(H // 32) % 4 != 1]
+    compare.assert_equal(small, np.full(small.shape, 127 - 117 - below, np.uint8), "scales")
+    got = codes.cpu().numpy()[:, ~big]
+    code = 0x7E if below else 0x78
+    compare.assert_equal(got, np.where(sign[:, ~big] < 0, code | 0x80, code).astype(np.uint8), "codes")
