@@ -327,7 +327,8 @@ moe_status moe_combine(const uint16_t* y, const float* topk_weights, const int32
  *   residual_out[t, :] = bf16(s)          (NULL: not written)
  *   out[t, :] = bf16(n)
  * Each result is rounded once, to nearest even: n is formed from the unrounded
- * s.  A row's result depends on H and the row alone, not on its batch.  A row with
+ * s, right to three fp32 steps whatever s / sqrt(..) is on the way.  A row's result
+ * depends on H and the row alone, not on its batch.  A row with
  * an infinity or a NaN normalises as the formula does (NaN at the infinities and
  * 0 beside them; a NaN makes the whole row NaN).
  * x, residual, residual_out, out bf16 [T, H]; weight bf16 [H].  H % 8 == 0,

@@ -12,12 +12,14 @@
 // sum of squares crosses lanes by DPP and waves by LDS, in an order that
 // depends on H alone, so a row's result does not depend on its batch.
 // The sum of squares and the root are formed in fp64, which has the range for
-// any fp32 square; n is then right to two fp32 steps.  An MXFP8 scale is a power
-// of two, decided by which power the block's maximum reaches, so a maximum that
-// near to one is looked at again in fp64: decided in fp32
-// about one block in six million took the neighbouring scale.  (All products in
-// fp64: 72.4 us instead of 70.0 at 8192 x 7168.)  n is rounded once in every format: codes are not taken
-// of a bf16 row.
+// any fp32 square, and so are the products of a vector whose s / rms falls below
+// fp32's normals (the look for one costs 0.1 us at one row, 0.2 of 69 at 8192 x
+// 7168); n is then right to three fp32 steps.  An MXFP8 scale is a power of two,
+// decided by which power the block's maximum reaches, so a maximum that near to
+// one is looked at again in fp64: decided in fp32 about one block in six million
+// took the neighbouring scale.  (All products in fp64: 72.4 us instead of 70.0 at
+// 8192 x 7168.)  n is rounded once in every format: codes are not taken of a bf16
+// row.
 #include "fp8_common.h"
 #include "kernels.h"
 
@@ -27,7 +29,7 @@ namespace {
 enum NormMode { kNormBf16 = 0, kNormFp8 = 1, kNormMx = 2 };
 
 constexpr uint32_t kInfBits = 0x7F800000u;
-// fp32 steps that n may be off by: two products and the factor's own rounding,
+// fp32 steps that n may be off by, at most 2.5: two products and the factor's own rounding,
 // half a step each, with room to spare.
 constexpr uint32_t kNear = 8;
 
@@ -63,6 +65,14 @@ __device__ __forceinline__ double row_sum(double v, double* s_part) {
         for (int w = 0; w < WPR; ++w) v += s_part[w];
     }
     return v;
+}
+
+// s * rstd * w in fp64, for the few vectors that need it.  The compiler shall not
+// know s and w: it would keep all of the row sum's conversions in registers until
+// here (8192 x 7168 MXFP8 76 us instead of 70) and convert every weight.
+__device__ __forceinline__ double product64(float s, double rstd, float w) {
+    asm("" : "+v"(s), "+v"(w));
+    return (double)s * rstd * (double)w;
 }
 
 template <int WPR, int NV, int MODE>
@@ -125,7 +135,19 @@ __global__ __launch_bounds__(kWave* WPR) void rmsnorm_kernel(const u32x4* __rest
         float f[8], n[8];
         unpack8(wv[i], f);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) n[e] = s[i][e] * pre * scaled * f[e];
+        for (int e = 0; e < 8; ++e) n[e] = s[i][e] * pre * scaled;
+        // a quotient below fp32's normals has lost bits that a large weight would
+        // bring back: then, and where it is 0, the vector's products in fp64
+        float least = fabsf(n[0]);
+#pragma unroll
+        for (int e = 1; e < 8; ++e) least = fminf(least, fabsf(n[e]));
+        if (__builtin_expect(least < 0x1p-126f, 0)) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) n[e] = (float)product64(s[i][e], rstd, f[e]);
+        } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) n[e] *= f[e];
+        }
         if (out != nullptr && c < n8) store_stream(out + base + c, pack8(n));
         if constexpr (MODE != kNormBf16) {
             // a scale group is gl consecutive lanes; H is a multiple of it, so
@@ -146,7 +168,7 @@ __global__ __launch_bounds__(kWave* WPR) void rmsnorm_kernel(const u32x4* __rest
                     uint32_t reaches = 0;
 #pragma unroll
                     for (int e = 0; e < 8; ++e)
-                        if (fabs((double)s[i][e] * rstd * (double)f[e]) >= reach) reaches = 1;
+                        if (fabs(product64(s[i][e], rstd, f[e])) >= reach) reaches = 1;
                     reaches = group_abs_max(reaches, gl);
                     if (near) b = block_scale(reaches ? edge : edge - 1, true);
                 }

@@ -56,6 +56,34 @@ def rmsnorm(x, r, w, eps):
 NORM_REL = 50 * FP32
 
 
+# What the kernel's steps add up to, with its row sum, division and root in fp64
+# (2^-46 together): x + r rounded, in s and at most as much in the rms of them, 1 /
+# rms rounded, two products: 5 * 2^-24, and half a step for the rest.
+NORM_STEPS_REL = 5.5 * FP32
+FP32_TINY = 2.0 ** -149   # a step of fp32's subnormals, which n may be among
+
+
+def norm_steps_bound(n) -> np.ndarray:
+    """Of bf16(n)."""
+    e = NORM_STEPS_REL * np.abs(n) + FP32_TINY
+    return e + BF16 * (np.abs(n) + e) + BF16_TINY
+
+
+def quantised_steps_bound(n, scale) -> np.ndarray:
+    """Of code * scale, scale per element and as stored.  The quotient that the code
+    is taken of differs from n / scale by n's steps, those of scale and of its
+    inverse and the product (3 half steps): 8.5 * 2^-24; half an E4M3 step of it
+    (2^-10 below its normals).  A subnormal scale is off by up to half of fp32's
+    least step, 448 times in the largest code."""
+    e = 9 * FP32 * np.abs(n) + 449 * FP32_TINY
+    return np.maximum(E4M3 * (np.abs(n) + e), 2.0 ** -10 * scale) + e
+
+
+def mx_exponent(amax) -> np.ndarray:
+    """max(floor(log2 amax) - 8, -127) of float64 block maxima."""
+    return np.where(amax > 0, np.maximum(np.frexp(amax)[1] - 9, -127), -127)
+
+
 def rmsnorm_bound(n) -> np.ndarray:
     return (BF16 + NORM_REL) * np.abs(n) * (1 + BF16) + BF16_TINY
 

@@ -8,6 +8,7 @@ import pytest
 
 import compare
 import gpu_util as G
+import plain64 as P
 from moe_glue_amd import inputs
 
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
@@ -39,7 +40,7 @@ def bits(a):
 @pytest.mark.parametrize("steps", [3, 4, 5, 6])
 def test_mxfp8_scale_of_a_maximum_just_below_2_128(dev, H, steps):
     """Half of a row is +-2, half +-1, so rms^2 = 5/2 + eps, and w = 1.6 * 2^127: eps
-    puts the maximum `steps` fp32 steps below 2^128.  n is right to two steps, so
+    puts the maximum `steps` fp32 steps below 2^128.  n is off by less than three, so
     it is finite and its scale that of a maximum below 2^128: 2^(127 - 8), the
     codes 448 (saturated) and 256 (255.99)."""
     import torch
@@ -102,3 +103,60 @@ def test_mxfp8_scale_where_x_times_w_falls_below_fp32(dev, below):
     got = codes.cpu().numpy()[:, ~big]
     code = 0x7E if below else 0x78
     compare.assert_equal(got, np.where(sign[:, ~big] < 0, code | 0x80, code).astype(np.uint8), "codes")
+
+
+def check_norm(dev, x, r, w, eps, fmt, group, what):
+    """A call on bf16 bits, every output against the 64-bit form."""
+    import torch
+    import moe_glue_amd as mg
+
+    T, H = x.shape
+    s, n = P.rmsnorm(x, r, w, eps)
+    xd, wd = G.to_dev(x, dev), G.to_dev(w, dev)
+    rd = None if r is None else G.to_dev(r, dev)
+    normed = torch.full((T, H), float("nan"), dtype=torch.bfloat16, device=dev)
+    if fmt == "bf16":
+        _, res = mg.rmsnorm(xd, wd, rd, eps, out=normed)
+    elif fmt == "fp8":
+        codes, scales, res = mg.rmsnorm_fp8(xd, wd, group, rd, eps, normed=normed)
+    else:
+        codes, scales, res = mg.rmsnorm_mxfp8(xd, wd, rd, eps, normed=normed)
+    torch.cuda.synchronize()
+    if r is not None:
+        compare.assert_equal(G.to_host(res), bits(s.astype(np.float32)), f"{what}: residual_out")
+    P.assert_within(P.f64(G.to_host(normed)), n, P.norm_steps_bound(n), f"{what}: out")
+    if fmt == "bf16":
+        return
+    b = n.reshape(T, -1, group)
+    amax = np.abs(b).max(-1)
+    q = P.e4m3_values(codes.cpu().numpy()).reshape(b.shape)
+    if fmt == "fp8":
+        sc = scales.cpu().numpy().astype(np.float64)
+        P.assert_within(sc, amax / 448, (P.NORM_STEPS_REL + P.FP32) * amax / 448 + P.FP32_TINY, f"{what}: scales")
+    else:
+        compare.assert_equal(scales.cpu().numpy().astype(int), P.mx_exponent(amax) + 127, f"{what}: scales")
+        sc = 2.0 ** P.mx_exponent(amax)
+        b = np.clip(b, -448 * sc[..., None], 448 * sc[..., None])
+    P.assert_within(q * sc[..., None], b, P.quantised_steps_bound(b, sc[..., None]), f"{what}: codes")
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("fmt,group", [("bf16", 0), ("fp8", 8), ("fp8", 64), ("mxfp8", 32)])
+@pytest.mark.parametrize("H", [256, 2112, 8256])
+@pytest.mark.parametrize("residual", [True, False])
+def test_norm_whose_quotient_falls_below_fp32(dev, fmt, group, H, residual):
+    """Small values beside large ones under large weights: s / rms is below fp32's
+    normals, or its whole range, n is not."""
+    print(f"[norm low] {fmt} group={group} H={H} residual={residual}", flush=True)
+    rng = np.random.default_rng([H, group, residual])
+    big = np.arange(H) // 32 % 4 == 1
+    w = np.where(big, 1.0, np.where(np.arange(H) % 2 == 0, 2.0 ** 100, 2.0 ** 127)) * rng.uniform(1, 1.9, H)
+    #       rms about 2^40    2^100         subnormal x     about 2^-126   neighbours large and small
+    rows = [(41.0, -100.0), (101.0, -120.0), (20.0, -130.0), (41.0, -86.0), (41.0, -100.0), (41.0, -100.0)]
+    x = np.stack([np.where(big, 2.0 ** hi, 2.0 ** lo) for hi, lo in rows])
+    x[4, 5::8] = 2.0 ** 41   # (their own weights large: n up to 2^128 / 4)
+    w[5::8] = np.minimum(w[5::8], 2.0 ** 100)
+    x[5, ::3] = 0
+    x = x * rng.uniform(1, 1.9, x.shape) * rng.choice([-1, 1], x.shape)
+    r = np.where(rng.random(x.shape) < 0.5, x * rng.uniform(-1, 1, x.shape), 0) if residual else None
+    check_norm(dev, bits(x), None if r is None else bits(r), bits(w), 1e-6, fmt, group, f"{fmt} {H}")
