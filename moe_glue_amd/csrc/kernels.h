@@ -203,8 +203,6 @@ hipError_t launch_mix_probe(const void* src, void* dst, uint32_t cycles, uint32_
                             int vectors_per_lane, int threads, hipStream_t stream);
 
 // ------------------------------------------------------------------- norm
-// Widest row: 16 waves of 8 16-byte vectors a lane.
-constexpr int kNormMaxWidth = MOE_NORM_H_MAX;
 struct NormArgs {
     const void* x;         // bf16 [T, H]
     const void* residual;  // bf16 [T, H] or null

@@ -291,7 +291,8 @@ hipError_t launch_linear_mxfp4(const void* x, int T, int K, const uint8_t* w, co
         const int rows = N <= 16 * kCus ? 1 : N <= 32 * kCus ? 2 : 4;  // one workgroup per CU as far as N reaches
         const auto nt = [&](auto r) {
             constexpr int R = decltype(r)::value;
-            if (T <= 16) return launch_wide<R, 1>(x, T, K, w, scales, N, y, stream);
+            if constexpr (R > 1)  // (with R = 1 the rows kernel has the batches up to 16)
+                if (T <= 16) return launch_wide<R, 1>(x, T, K, w, scales, N, y, stream);
             if (T <= 32) return launch_wide<R, 2>(x, T, K, w, scales, N, y, stream);
             return launch_wide<R, 4>(x, T, K, w, scales, N, y, stream);
         };

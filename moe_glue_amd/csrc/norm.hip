@@ -236,6 +236,7 @@ hipError_t launch_rmsnorm(const NormArgs& a, hipStream_t stream) {
         default: break;
     }
     if (waves <= 16) return launch_shape<16, 2>(a, stream);
+    static_assert(16 * 8 * kWave * 8 == MOE_NORM_H_MAX, "the widest row: 16 waves of 8 vectors a lane");
     return launch_shape<16, 8>(a, stream);
 }
 
