@@ -49,17 +49,17 @@ def rmsnorm(x, r, w, eps):
     return s, n
 
 
-# Relative error of the kernel's fp32 n: a lane adds at most 64 squares in turn,
-# then 6 lane steps and 16 waves (86 roundings, halved by the square root),
+# Relative error of n where every step is fp32: a lane adds at most 64 squares in
+# turn, then 6 lane steps and 16 waves (86 roundings, halved by the square root),
 # the square's own factor s and the division, root, quotient and two products
-# (7 more): 50 * 2^-24.
+# (7 more): 50 * 2^-24.  The kernel's steps are held to NORM_STEPS_REL below.
 NORM_REL = 50 * FP32
 
 
-# What the kernel's steps add up to, with its row sum, division and root in fp64
-# (2^-46 together): x + r rounded, in s and at most as much in the rms of them, 1 /
-# rms rounded, two products: 5 * 2^-24, and half a step for the rest.
-NORM_STEPS_REL = 5.5 * FP32
+# What the kernel's steps add up to from s = fp32(x + r) on, with its row sum,
+# division and root in fp64 (2^-46 together): 1 / rms rounded and two products,
+# 3 * 2^-24, and half a step for the rest.
+NORM_STEPS_REL = 3.5 * FP32
 FP32_TINY = 2.0 ** -149   # a step of fp32's subnormals, which n may be among
 
 
@@ -72,10 +72,10 @@ def norm_steps_bound(n) -> np.ndarray:
 def quantised_steps_bound(n, scale) -> np.ndarray:
     """Of code * scale, scale per element and as stored.  The quotient that the code
     is taken of differs from n / scale by n's steps, those of scale and of its
-    inverse and the product (3 half steps): 8.5 * 2^-24; half an E4M3 step of it
+    inverse and the product (3 half steps): 6.5 * 2^-24; half an E4M3 step of it
     (2^-10 below its normals).  A subnormal scale is off by up to half of fp32's
     least step, 448 times in the largest code."""
-    e = 9 * FP32 * np.abs(n) + 449 * FP32_TINY
+    e = 7 * FP32 * np.abs(n) + 449 * FP32_TINY
     return np.maximum(E4M3 * (np.abs(n) + e), 2.0 ** -10 * scale) + e
 
 
@@ -140,6 +140,40 @@ def layer(x, ids, weights, wgu, wd):
         np.add.at(out, ts, wj * y)
         np.add.at(bound, ts, wj * (dy + (2.0 ** -20 + k * 2 * FP32) * mag))
     return out, bound + BF16 * (np.abs(out) + bound) + BF16_TINY
+
+
+def round_bf16(v) -> np.ndarray:
+    """Float64 -> the nearest bf16's value, through fp32 as the kernels do."""
+    b = np.asarray(v, np.float64).astype(np.float32).view(np.uint32).astype(np.uint64)
+    b = (b + np.uint64(0x7FFF) + ((b >> np.uint64(16)) & np.uint64(1))) & np.uint64(0xFFFF0000)
+    return b.astype(np.uint32).view(np.float32).astype(np.float64)
+
+
+def layer_pair(x, ids, weights, wgu, wd):
+    """(exact, rounded): the layer without a rounding, and with the two that the
+    calls document, of act and of out, to bf16."""
+    xv = f64(x)
+    exact, rounded = np.zeros(xv.shape), np.zeros(xv.shape)
+    I = wd.shape[2]
+    for e in np.unique(ids):
+        ts, js = np.nonzero(ids == e)
+        h = xv[ts] @ wgu[e].T
+        act = h[:, :I] / (1.0 + np.exp(-h[:, :I])) * h[:, I:]
+        wj, d = weights[ts, js][:, None], wd[e].T
+        np.add.at(exact, ts, wj * (act @ d))
+        np.add.at(rounded, ts, wj * (round_bf16(act) @ d))
+    return exact, round_bf16(rounded)
+
+
+def assert_as_precise(got, exact, rounded, what):
+    """got's rms error is that of `rounded`, the exact values with the documented
+    roundings.  Against those, 2^-8 at most and 2^-9.8 in the rms, fp32's own errors
+    (2^-24 a step, some sqrt(K) of them) vanish, and the sums of a correct kernel
+    round as the model's do but for values next to a tie: a tenth more covers it.
+    One more bf16 rounding of h or y, or a lost column, adds a fifth at least."""
+    got = np.asarray(got, np.float64)
+    err, ref = (np.sqrt(np.mean((v - exact) ** 2)) for v in (got, rounded))
+    assert err <= 1.1 * ref, f"{what}: rms error {err:.4g}, {err / ref:.2f} times that of the documented roundings"
 
 
 def assert_within(got, want, bound, what):

@@ -1,5 +1,6 @@
-"""The norm at the ends of its range: the largest batch, and values whose steps
-leave fp32's range although the result does not."""
+"""The norm held to the rounding of its own steps (plain64.NORM_STEPS_REL), and at
+the ends of its range: the largest batch, and values whose steps leave fp32's range
+although the result does not."""
 import os
 import subprocess
 
@@ -111,7 +112,8 @@ def check_norm(dev, x, r, w, eps, fmt, group, what):
     import moe_glue_amd as mg
 
     T, H = x.shape
-    s, n = P.rmsnorm(x, r, w, eps)
+    s = (P.f64(x) + (0.0 if r is None else P.f64(r))).astype(np.float32).astype(np.float64)
+    n = s / np.sqrt(np.mean(s * s, axis=-1, keepdims=True) + np.float64(np.float32(eps))) * P.f64(w)
     xd, wd = G.to_dev(x, dev), G.to_dev(w, dev)
     rd = None if r is None else G.to_dev(r, dev)
     normed = torch.full((T, H), float("nan"), dtype=torch.bfloat16, device=dev)
@@ -160,3 +162,22 @@ def test_norm_whose_quotient_falls_below_fp32(dev, fmt, group, H, residual):
     x = x * rng.uniform(1, 1.9, x.shape) * rng.choice([-1, 1], x.shape)
     r = np.where(rng.random(x.shape) < 0.5, x * rng.uniform(-1, 1, x.shape), 0) if residual else None
     check_norm(dev, bits(x), None if r is None else bits(r), bits(w), 1e-6, fmt, group, f"{fmt} {H}")
+
+
+NORM_SIZES = [("bf16", 0, 1, 8), ("bf16", 0, 7, 520), ("bf16", 0, 40, 2048), ("bf16", 0, 9, 8200), ("bf16", 0, 2, 65536),
+              ("fp8", 8, 3, 24), ("fp8", 128, 40, 2048), ("fp8", 512, 9, 7168), ("fp8", 64, 3, 16448),
+              ("mxfp8", 32, 3, 96), ("mxfp8", 32, 40, 2048), ("mxfp8", 32, 9, 7168), ("mxfp8", 32, 2, 65536)]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("fmt,group,T,H", NORM_SIZES)
+@pytest.mark.parametrize("residual", [True, False])
+def test_norm_is_right_to_its_roundings(dev, fmt, group, T, H, residual):
+    """Rows from 2^-60 to 2^60: the scales, which are not rounded to 8 bits, see an
+    error of a few fp32 steps in the row's sum."""
+    print(f"[norm steps] {fmt} group={group} {T}x{H} residual={residual}", flush=True)
+    rng = np.random.default_rng([T, H, group, residual])
+    row = 2.0 ** np.linspace(-60, 60, T)[:, None]
+    x = bits(row * rng.standard_normal((T, H)))
+    r = bits(4 * row * rng.standard_normal((T, H))) if residual else None
+    check_norm(dev, x, r, bits(rng.standard_normal(H)), 1e-30, fmt, group, f"{fmt} {T}x{H}")
