@@ -52,9 +52,20 @@ def _torch():
     return _torch_module
 
 
+_raw_stream = None
+
+
 def _stream(device) -> int:
     """Handle of torch's current stream on `device`."""
-    return _torch()._C._cuda_getCurrentRawStream(device.index)
+    global _raw_stream
+    if _raw_stream is None:
+        # torch's own getter of the handle makes no stream object on the way (0.12 us
+        # a call, 1.87 with one), but torch does not promise it: without it the
+        # documented one
+        torch = _torch()
+        _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+            lambda index: torch.cuda.current_stream(index).cuda_stream)
+    return _raw_stream(device.index)
 
 
 def _ptr(t) -> int:
