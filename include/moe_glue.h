@@ -360,7 +360,14 @@ moe_status moe_rmsnorm_fp8(const uint16_t* x, const uint16_t* residual, const ui
  * E4M3(clamp(n / 2^e, +-448))).  A
  * block with a NaN or an infinity in n has the scale byte 255 (NaN) and codes
  * 0x7F.  codes uint8 [T, H]; scales uint8 [T, H/32]; H % 32 == 0; otherwise as
- * moe_rmsnorm_fp8. */
+ * moe_rmsnorm_fp8.
+ *
+ * To the experts' order the codes and scales of either norm go through
+ * moe_expand_rows, a copy of whole rows bit for bit: a row of b bytes is one of
+ * b/2 columns to it, and b has to be a multiple of 16 (codes: H % 16 == 0; fp32
+ * scales: H / group % 4 == 0; E8M0: H % 512 == 0).  That differs from
+ * moe_expand_rows_fp8 / _mxfp8 of the bf16 row in the rounding to bf16 that those
+ * quantise after. */
 moe_status moe_rmsnorm_mxfp8(const uint16_t* x, const uint16_t* residual, const uint16_t* weight, int32_t T, int32_t H,
                              float eps, uint16_t* residual_out, uint16_t* out, uint8_t* codes, uint8_t* scales,
                              void* stream);
