@@ -384,8 +384,9 @@ moe_status moe_rmsnorm_mxfp8(const uint16_t* x, const uint16_t* residual, const 
  *   act     = bf16(silu(g) * u)
  *   y_j     = w_down[e] act          (fp32)
  *   out[t]  = bf16(sum_j topk_weights[t, j] * y_j)   (fp32, in j order)
- * act is rounded because the second product takes bf16 operands; nothing else
- * is, before out.  Reads the weights of the experts that the batch picks, once
+ * silu(g) = g / (1 + e^-g), to 2^-17 of its value and 2^-118 (it is 0 from about
+ * g = -87 on).  act is rounded because the second product takes bf16 operands;
+ * nothing else is, before out.  Reads the weights of the experts that the batch picks, once
  * each.  The same call gives the same bits every time.
  * Layouts: logits fp32 [T, E], bias fp32 [E] or NULL, x bf16 [T, H], w_gate_up
  * bf16 [E, 2I, H], w_down bf16 [E, H, I], topk_ids int32 [T, k], topk_weights

@@ -96,6 +96,46 @@ def test_layer_paths(dev, fmt, E, k, H, I, T, kind):
     P.assert_as_precise(got, *P.layer_pair(x, ids, w, Values(*gu), Values(*dn)), what)
 
 
+@pytest.mark.gpu
+@pytest.mark.parametrize("fmt", ["bf16", "mxfp4"])
+def test_layer_silu_over_its_range(dev, fmt):
+    """Experts that take g and u from columns 0 and 1 of x and hand act on: g from
+    -3e38 to 3e38, u small and large.  silu is right to 2^-17 of its value (g log2 e
+    up to 128 rounds by 2^-18, as its constant does) and 2^-118."""
+    import torch
+    import moe_glue_amd as mg
+
+    T, E, k, H, I = 64, 2, 1, 32, 32
+    g = np.concatenate([-np.logspace(-3, 38.4, 40), [-86, -87, -87.5, -88, -89, -100, -150, 0], np.logspace(-3, 30, 16)])
+    u = np.resize([1.0, -3e7, 2e-6, 1e30, -1e-30], T)
+    x = np.zeros((T, H))
+    x[:, 0], x[:, 1] = g, u
+    x = inputs.f32_to_bf16_bits(x.astype(np.float32))
+    if fmt == "bf16":
+        gu, dn = np.zeros((E, 2 * I, H), np.uint16), np.zeros((E, H, I), np.uint16)
+        gu[:, 0, 0] = gu[:, I, 1] = dn[:, :, 0] = 0x3F80
+        w, call = (gu, dn), mg.decode_layer
+    else:
+        gu, dn = np.zeros((E, 2 * I, H // 2), np.uint8), np.zeros((E, H, I // 2), np.uint8)
+        gu[:, 0, 0], gu[:, I, 0], dn[:, :, 0] = 0x02, 0x20, 0x02
+        one = lambda *s: np.full(s, 127, np.uint8)  # noqa: E731
+        w, call = (gu, one(E, 2 * I, 1), dn, one(E, H, 1)), mg.decode_layer_mxfp4
+    logits = np.zeros((T, E), np.float32)
+    r = call(G.to_dev(logits, dev), k, G.to_dev(x, dev), *(G.to_dev(v, dev) for v in w))
+    torch.cuda.synchronize()
+    got = P.f64(G.to_host(r["out"]))
+    g, u = P.f64(x[:, 0]), P.f64(x[:, 1])
+    with np.errstate(over="ignore"):
+        silu = g / (1 + np.exp(-g))
+    want = silu * u
+    e = (2.0 ** -17 * np.abs(silu) + 2.0 ** -118) * np.abs(u) + P.BF16_TINY
+    bound = e + 2 * P.BF16 * (np.abs(want) + e) + P.BF16_TINY  # act's rounding (out's repeats it)
+    fits = np.abs(want) < 3.38e38
+    assert fits.sum() > 50
+    P.assert_within(got[fits], np.repeat(want[fits, None], H, 1), np.repeat(bound[fits, None], H, 1), "silu")
+    assert np.isinf(got[~fits]).all()
+
+
 # --------------------------------------------------------------------- linear
 # Every instance of both kernels; the staged one (R = 1, 2, 4 row tiles to N = 4096,
 # 8192 and beyond; 16, 32 or 64 tokens) keeps 8, 4 or 2 chunks of 256 k in flight and
