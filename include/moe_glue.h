@@ -387,7 +387,8 @@ moe_status moe_rmsnorm_mxfp8(const uint16_t* x, const uint16_t* residual, const 
  * silu(g) = g / (1 + e^-g), to 2^-17 of its value and 2^-118 (it is 0 from about
  * g = -87 on).  act is rounded because the second product takes bf16 operands;
  * nothing else is, before out.  Reads the weights of the experts that the batch picks, once
- * each.  The same call gives the same bits every time.
+ * for every 16 (MXFP4: 8) tokens of theirs.  The same call gives the same bits every
+ * time.
  * Layouts: logits fp32 [T, E], bias fp32 [E] or NULL, x bf16 [T, H], w_gate_up
  * bf16 [E, 2I, H], w_down bf16 [E, H, I], topk_ids int32 [T, k], topk_weights
  * fp32 [T, k], out bf16 [T, H].  H % 8 == 0 and I % 8 == 0; x, the weights, out

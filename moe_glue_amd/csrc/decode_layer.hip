@@ -5,9 +5,10 @@
 //   2  y[p, :] = Wd[e] act[p, :];  out[t, :] = bf16(sum_j w[t,j] y[p(t,j), :])
 //
 // p numbers the (expert, token) pairs by expert, then token.  Bound by the
-// stream of the picked experts' weights, each read once: a few tokens per
-// expert are far too little arithmetic to matter, so every kernel is built
-// round loads in flight, with the products on the matrix cores (mfma_rows.h).
+// stream of the picked experts' weights, each read once for every entry (16 or 8 of
+// an expert's tokens): a few tokens per expert are far too little arithmetic to
+// matter, so every kernel is built round loads in flight, with the products on the
+// matrix cores (mfma_rows.h).
 //
 // Launch 1.  No workgroup waits for another, so each recomputes the routing in
 // LDS (as the one-launch dispatch does; about 4 us) and then walks its share of
@@ -23,12 +24,14 @@
 // and split K when there are few.  fp32 y meets in LDS and is summed over j in
 // order, so the same call always gives the same bits.
 //
-// Measured (us, launch 1 + launch 2; the weights read at the rate of a large
-// streaming read, 6.7 TB/s, in brackets): one token, 128 experts of 2048 x 768,
-// bf16, 12.1 + 6.8 (11.3 together); 32 tokens 116 + 58 (155); 8 tokens, some 42 of
-// 64 experts of 7168 x 2048, bf16, 347 + 169 (550); 16 tokens, 256 experts of 7168 x
-// 2048, MXFP4, 228 + 128 (285); 61 tokens, skewed, 64 experts of 4096 x 1408,
-// MXFP4, 86 + 51 (47; here the columns' loads and the products count too).
+// Measured (us, launch 1 + launch 2, medians of 27 dispatches under rocprofv3's
+// kernel trace, of several runs; the weights read at the rate of a large streaming
+// read, 6.7 TB/s, in brackets): one token, 128 experts of 2048 x 768, bf16, 13.6 to
+// 14.5 + 6.8 to 7.3 (11.3 together), MXFP4 11.2 + 7.9 (3.0); 32 tokens, bf16, 119 to
+// 120 + 60 (155), MXFP4 43 + 35 (42); 8 tokens, some 42 of 64 experts of 7168 x 2048,
+// bf16, 366 + 180 (550); of 256 such experts, MXFP4, one token 29.6 + 21.1 (28), 16
+// tokens 234 to 239 + 128 to 132 (285); 61 tokens, skewed, 64 experts of 4096 x 1408,
+// MXFP4, 87 to 90 + 52 to 53 (47; here the columns' loads and the products count too).
 #include "kernels.h"
 #include "mfma_rows.h"
 #include "route_common.h"
@@ -52,7 +55,7 @@ constexpr int kEntryTokens = 16;
 template <>
 constexpr int kEntryTokens<Mxfp4Weights> = 8;  // by registers, see mfma_rows.h
 constexpr int kMaxEntries = kEMax + kMaxSlots / 8;
-// Weights are streamed past the caches (decode workload 132 -> 120 and 65 -> 61
+// Weights are streamed past the caches (decode workload 132 -> 120 and 65 -> 60
 // us, DeepSeek-V3-shaped MXFP4 247 -> 234 and 134 -> 129), except under entries
 // as wide as they come: the expert may have another, which reads them again
 // (skewed MXFP4 98 -> 86 and 55 -> 52).
@@ -403,7 +406,7 @@ __global__ __launch_bounds__(kThreads) void decode_down_kernel(int T, int k, con
         const DownTask t[1] = {task_of(a)};
         // two small entries at a time: a wave with short rows would wait out the
         // memory's latency after every few loads (MXFP4, 32 tokens, 2048 x 768 38.0
-        // -> 34.2 us, 1024 x 2048 45 -> 40; not for bf16 rows, 58 -> 61 us)
+        // -> 34.2 us, 1024 x 2048 45 -> 40; not for bf16 rows, 60 -> 63 us)
         if (PAIRS && parts == 1 && task + kWaves < n && t[0].end - t[0].p0 <= 4) {
             const DownTask two[2] = {t[0], task_of(task + kWaves)};
             if (two[1].end - two[1].p0 <= 4) {
@@ -444,8 +447,8 @@ __global__ __launch_bounds__(kThreads) void decode_down_kernel(int T, int k, con
 constexpr int kWideDown = 3584;
 
 // One workgroup per CU, its 8 waves with up to 256 registers each.  Two of half
-// the registers: decode workload 117 -> 121 us, DeepSeek-V3-shaped MXFP4, which
-// then spills, 235 -> 299 us.
+// the registers: decode workload 120 -> 135 us, DeepSeek-V3-shaped MXFP4, which
+// then spills, 234 -> 316 us.
 constexpr int kMaxGrid = 256;
 
 template <class W, int G, int V>

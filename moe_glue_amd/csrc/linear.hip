@@ -133,7 +133,8 @@ __global__ __launch_bounds__(kThreads) void linear_mxfp4_wide_kernel(const uint1
     uint8_t sv[kAhead];
     const auto fetch_w = [&](auto index, int chunk) {
         constexpr int j = decltype(index)::value;
-        // past K: zeros (codes of zero under scale byte 0)
+        // past K: zeros (codes of zero under scale byte 0).  With R < 4 several waves
+        // load the same piece, and the first of them stages it.
         const bool in_w = chunk * kChunk + w_piece * 32 < K;
         wv[j] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(
                                               wb, (int)(in_w ? w_at : kNowhere), chunk * (kChunk / 2), kCacheNt));
@@ -195,7 +196,7 @@ __global__ __launch_bounds__(kThreads) void linear_mxfp4_wide_kernel(const uint1
     // c + 2 takes chunk c's buffer, and its registers chunk c + 2 + kAhead.
     const auto step = [&](auto index, int chunk) {
         constexpr int buf = decltype(index)::value % 2;
-        const int next = min(chunk + 2 + kAhead, chunks - 1);
+        const int next = min(chunk + 2 + kAhead, chunks - 1);  // (behind the last: the last again, not used)
         const auto products = [&](int r) {
             const bf16x8 a = Mxfp4Weights::values<0>(u32x2{codes[buf][r], 0u},
                                                      __builtin_bit_cast(float, scale[buf][r] << 23));
@@ -286,6 +287,7 @@ hipError_t launch_linear_mxfp4(const void* x, int T, int K, const uint8_t* w, co
     // 10.6, 9.9 / 11.3, 9.7 / 14.7, 16.7 / 20.7; 7168 x 4096 7.8 / 11.1, 10.2 / 11.9,
     // 17.7 / 15.5, 34 / 21.6; 2048 x 7168 7.4 / 6.9, 9.5 / 7.0, 15.1 / 8.0, 25 / 11.1;
     // 7168 x 16384 (T = 4: 15.8 / 18) 26 / 18.4, 36 / 19.6, 67 / 22.7, 129 / 27.7.
+    // The rule goes by N and T alone; K was not varied at one N.
     const int from = N <= 8 * kCus ? MOE_DECODE_T_MAX : N <= 16 * kCus ? 16 : N <= 32 * kCus ? 8 : 4;
     if (T > from) {
         const int rows = N <= 16 * kCus ? 1 : N <= 32 * kCus ? 2 : 4;  // one workgroup per CU as far as N reaches

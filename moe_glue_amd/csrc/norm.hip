@@ -6,7 +6,7 @@
 //   out = bf16(n), or E4M3 codes of n with fp32 or E8M0 block scales
 //
 // Bound by HBM: about 6 operations for 6 to 8 bytes (8192 x 7168 with residual
-// and MXFP8 out moves 412 MB in 70 us, 5.9 TB/s).  A row stays in
+// and MXFP8 out moves 412 MB in 69 us, 6.0 TB/s).  A row stays in
 // registers from its load to its store, so x and r are read once.  One
 // workgroup takes one row with WPR waves of NV 16-byte vectors a lane; the
 // sum of squares crosses lanes by DPP and waves by LDS, in an order that
@@ -29,8 +29,8 @@ namespace {
 enum NormMode { kNormBf16 = 0, kNormFp8 = 1, kNormMx = 2 };
 
 constexpr uint32_t kInfBits = 0x7F800000u;
-// fp32 steps that n may be off by, at most 2.5: two products and the factor's own rounding,
-// half a step each, with room to spare.
+// fp32 steps that n may be off by, 2.5 at most (two products and the factor's own
+// rounding), with room to spare.
 constexpr uint32_t kNear = 8;
 
 // Sum over the 64 lanes of a wave, in every lane.
@@ -218,11 +218,10 @@ hipError_t launch_shape(const NormArgs& a, hipStream_t stream) {
 }  // namespace
 
 hipError_t launch_rmsnorm(const NormArgs& a, hipStream_t stream) {
-    // Two vectors a lane, as many waves as that takes: at 4096 x 2048 bf16 12.8 us
-    // (one vector and twice the waves 13.5, four and half 12.8), 1023 x 4096 FP8
-    // 8.3 (9.1, 9.0), 8192 x 7168 MXFP8 68.1 (four waves of four 69.7, fourteen of
-    // one 71.8); one row of 2048 1.9 (1.7, 2.2).  Rows past 8192 columns take
-    // sixteen waves.
+    // Two vectors a lane, as many waves as that takes (medians): at 4096 x 2048 bf16
+    // 13.2 us (one vector and twice the waves 13.4, four and half 13.1), 1023 x 4096
+    // FP8 9.1 (9.9, 9.9), 8192 x 7168 MXFP8 69.2 (77.2, 70.4); one row of 2048 2.1
+    // (1.9, 2.5).  Rows past 8192 columns take sixteen waves.
     const int waves = (a.H / 8 + 2 * kWave - 1) / (2 * kWave);
     switch (waves) {
         case 1: return launch_shape<1, 2>(a, stream);
