@@ -327,10 +327,10 @@ moe_status moe_combine(const uint16_t* y, const float* topk_weights, const int32
  *   residual_out[t, :] = bf16(s)          (NULL: not written)
  *   out[t, :] = bf16(n)
  * Each result is rounded once, to nearest even: n is formed from the unrounded
- * s, right to three fp32 steps whatever s / sqrt(..) is on the way.  A row's result
- * depends on H and the row alone, not on its batch.  A row with
- * an infinity or a NaN normalises as the formula does (NaN at the infinities and
- * 0 beside them; a NaN makes the whole row NaN).
+ * s, right to three fp32 steps whatever s / sqrt(..) is on the way.  A row's
+ * result depends on H and the row alone, not on its batch.  A row with an infinity
+ * or a NaN normalises as the formula does (NaN at the infinities and 0 beside
+ * them; a NaN makes the whole row NaN).
  * x, residual, residual_out, out bf16 [T, H]; weight bf16 [H].  H % 8 == 0,
  * H <= MOE_NORM_H_MAX; every pointer 16-byte aligned.  eps must be finite and
  * a positive normal fp32.  residual_out may be the very buffer residual (the
@@ -357,9 +357,8 @@ moe_status moe_rmsnorm_fp8(const uint16_t* x, const uint16_t* residual, const ui
 /* moe_rmsnorm with MXFP8 output: n (fp32) quantised per 32 consecutive columns
  * in the format of moe_expand_rows_mxfp8 (E8M0 scale byte e + 127,
  * e = max(floor(log2 amax) - 8, -127) of the unrounded maximum, codes
- * E4M3(clamp(n / 2^e, +-448))).  A
- * block with a NaN or an infinity in n has the scale byte 255 (NaN) and codes
- * 0x7F.  codes uint8 [T, H]; scales uint8 [T, H/32]; H % 32 == 0; otherwise as
+ * E4M3(clamp(n / 2^e, +-448))).  A block with a NaN or an infinity in n has the
+ * scale byte 255 (NaN) and codes 0x7F.  codes uint8 [T, H]; scales uint8 [T, H/32]; H % 32 == 0; otherwise as
  * moe_rmsnorm_fp8.
  *
  * To the experts' order the codes and scales of either norm go through
@@ -385,10 +384,10 @@ moe_status moe_rmsnorm_mxfp8(const uint16_t* x, const uint16_t* residual, const 
  *   y_j     = w_down[e] act          (fp32)
  *   out[t]  = bf16(sum_j topk_weights[t, j] * y_j)   (fp32, in j order)
  * silu(g) = g / (1 + e^-g), to 2^-17 of its value and 2^-118 (it is 0 from about
- * g = -87 on).  act is rounded because the second product takes bf16 operands;
- * nothing else is, before out.  Reads the weights of the experts that the batch picks, once
- * for every 16 (MXFP4: 8) tokens of theirs.  The same call gives the same bits every
- * time.
+ * g = -87 down).  act is rounded because the second product takes bf16 operands;
+ * nothing else is, before out.  Reads the weights of the experts that the batch
+ * picks, once for every 16 (MXFP4: 8) tokens of theirs.  The same call gives the
+ * same bits every time.
  * Layouts: logits fp32 [T, E], bias fp32 [E] or NULL, x bf16 [T, H], w_gate_up
  * bf16 [E, 2I, H], w_down bf16 [E, H, I], topk_ids int32 [T, k], topk_weights
  * fp32 [T, k], out bf16 [T, H].  H % 8 == 0 and I % 8 == 0; x, the weights, out
