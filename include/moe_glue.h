@@ -22,6 +22,12 @@
  *                    products included, on bf16 weights;
  *                    moe_decode_layer_mxfp4 on 4-bit weights
  *   moe_linear_mxfp4 product of a few tokens with 4-bit weights
+ *   moe_grouped_linear  rows in expert order times their experts' weights, with
+ *                    bias, SwiGLU and residual, bf16 (moe_grouped_linear_mxfp8:
+ *                    MXFP8); without segments a dense product
+ *   moe_grouped_linear_grad_x, moe_grouped_linear_grad_w  its gradients
+ *   moe_swiglu_backward, moe_combine_backward, moe_expand_rows_backward,
+ *   moe_route_backward  the gradients of the other steps
  *
  * The problem statement these calls follow:
  *   - "CuTeDSL at Perplexity" (Perplexity blog), section "Mixture of Experts
@@ -430,6 +436,133 @@ moe_status moe_decode_layer_mxfp4(const float* logits, const float* bias, int32_
  * MOE_ERR_SHAPE, MOE_ERR_ALIGN, MOE_ERR_UNSUPPORTED (T, K, N), MOE_ERR_HIP. */
 moe_status moe_linear_mxfp4(const uint16_t* x, int32_t T, int32_t K, const uint8_t* w, const uint8_t* scales,
                             int32_t N, uint16_t* y, void* stream);
+
+/* ------------------------------------------------------ experts' products */
+
+#define MOE_GROUPED_WIDTH_MAX (1 << 20) /* N and K of the grouped products        */
+#define MOE_GROUPED_TILES_MAX (1 << 22) /* tiles of one call, see moe_grouped_linear */
+
+typedef enum moe_act {
+    MOE_ACT_NONE = 0,
+    MOE_ACT_SWIGLU = 1 /* columns 0..N/2-1 are gates, the others ups, as moe_swiglu */
+} moe_act;
+
+/* Rows in expert order (as moe_expand_rows leaves them) times their experts'
+ * weights.  Rows r of expert e are expert_offsets[e] <= r < expert_offsets[e] +
+ * n_e, n_e = expert_counts[e], or up to expert_offsets[e+1] where expert_counts is
+ * NULL; for them, in fp32,
+ *   h = x[r, :] w[e]^T + bias[e]
+ *   pre[r, :] = bf16(h)                               (NULL: not written)
+ *   out[r, :] = bf16(act(h) + residual[r, :])
+ * with act(h) = h (MOE_ACT_NONE, out has N columns) or silu(g) u of h = (g | u)
+ * (MOE_ACT_SWIGLU, out has N/2 columns; silu as in moe_swiglu, of the unrounded h).
+ * Each result is rounded once, to nearest even.  A row's result depends on the row
+ * and its expert, and on how many rows the expert has only in the order of its
+ * fp32 sums.  The same call gives the same bits every time.
+ * Rows of no segment are neither read nor written: with the padded layout of
+ * moe_route_padded give its expert_counts, or the padding rows are computed like
+ * any other.  Segments must not overlap; entries outside [0, R] are taken as the
+ * nearest end, so bad ones give wrong rows but touch nothing outside the buffers.
+ * expert_offsets NULL: one expert has all R rows (E = 1, expert_counts NULL): a
+ * dense product, of a shared expert say.
+ * x bf16 [R, K]; expert_offsets int32 [E+1]; expert_counts int32 [E] or NULL;
+ * w bf16 [E, N, K] (with MOE_ACT_SWIGLU gate rows, then up rows); bias bf16 [E, N]
+ * or NULL; residual bf16, of out's shape, or NULL: it may be the very buffer out;
+ * pre bf16 [R, N] or NULL, with MOE_ACT_SWIGLU alone; out bf16 [R, N] or [R, N/2].
+ * K % 8 == 0, out's columns % 8 == 0; every bf16 pointer 16-byte aligned, offsets
+ * and counts 4-byte.  1 <= E <= MOE_E_MAX; N, K <= MOE_GROUPED_WIDTH_MAX; at most
+ * MOE_GROUPED_TILES_MAX tiles of 256 rows by 256 columns of w's rows: (R / 256 +
+ * min(E, R)) * ceil(N / 256).  R = 0 is a no-op.  Errors: MOE_ERR_NULL,
+ * MOE_ERR_SHAPE, MOE_ERR_ALIGN, MOE_ERR_UNSUPPORTED, MOE_ERR_HIP. */
+moe_status moe_grouped_linear(const uint16_t* x, int32_t R, const int32_t* expert_offsets,
+                              const int32_t* expert_counts, const uint16_t* w, int32_t E, int32_t N, int32_t K,
+                              const uint16_t* bias, moe_act act, const uint16_t* residual, uint16_t* pre,
+                              uint16_t* out, void* stream);
+
+/* moe_grouped_linear on MXFP8 rows (as moe_expand_rows_mxfp8 and
+ * moe_rmsnorm_mxfp8 give them) and MXFP8 weights: E4M3 codes and one E8M0 scale
+ * byte per 32 consecutive columns, a value being code * 2^(scale - 127) (scale
+ * byte 255, and the codes 0x7F and 0xFF: NaN).  The matrix cores take codes and
+ * scales as they are; nothing is rounded before out (and pre).
+ * x uint8 [R, K], x_scales uint8 [R, K/32], w uint8 [E, N, K], w_scales uint8
+ * [E, N, K/32]; K % 32 == 0; codes 16-byte aligned, scales at any byte.  Otherwise
+ * as moe_grouped_linear. */
+moe_status moe_grouped_linear_mxfp8(const uint8_t* x, const uint8_t* x_scales, int32_t R,
+                                    const int32_t* expert_offsets, const int32_t* expert_counts, const uint8_t* w,
+                                    const uint8_t* w_scales, int32_t E, int32_t N, int32_t K, const uint16_t* bias,
+                                    moe_act act, const uint16_t* residual, uint16_t* pre, uint16_t* out,
+                                    void* stream);
+
+/* The gradient of moe_grouped_linear's product to its rows: dx[r, :] =
+ * bf16(dy[r, :] w[e]) for the rows of each segment (the others are left as they
+ * are), dy being the gradient of h.  dy bf16 [R, N]; w bf16 [E, N, K]; dx bf16
+ * [R, K]; N % 8 == 0 and K % 8 == 0.  Tiles: those of moe_grouped_linear with
+ * ceil(K / 256).  R = 0 is a no-op.  Otherwise as moe_grouped_linear. */
+moe_status moe_grouped_linear_grad_x(const uint16_t* dy, int32_t R, const int32_t* expert_offsets,
+                                     const int32_t* expert_counts, const uint16_t* w, int32_t E, int32_t N, int32_t K,
+                                     uint16_t* dx, void* stream);
+
+/* The gradients of moe_grouped_linear's product to weights and bias, the sums
+ * running over each expert's rows in fp32:
+ *   dw[e, n, :] = sum_r dy[r, n] x[r, :]      (bf16, rounded once, or fp32)
+ *   dbias[e, n] = sum_r dy[r, n]              (fp32; NULL: not written)
+ * An expert without rows gets zeros, also with R = 0.  dy bf16 [R, N]; x bf16
+ * [R, K]; dw [E, N, K], bf16, or fp32 with dw_fp32 != 0; dbias fp32 [E, N].
+ * N % 8 == 0 and K % 8 == 0; dy, x and dw 16-byte aligned, dbias 4-byte.  At most
+ * MOE_GROUPED_TILES_MAX tiles of 128 by 128: E * ceil(N / 128) * ceil(K / 128).
+ * The same call gives the same bits every time.  Errors as moe_grouped_linear. */
+moe_status moe_grouped_linear_grad_w(const uint16_t* dy, const uint16_t* x, int32_t R, const int32_t* expert_offsets,
+                                     const int32_t* expert_counts, int32_t E, int32_t N, int32_t K, int32_t dw_fp32,
+                                     void* dw, float* dbias, void* stream);
+
+/* ------------------------------------------- gradients of the other steps */
+
+/* Of moe_swiglu: with s = 1 / (1 + e^-g) of h's gate columns, in fp32,
+ *   dh[r, i]     = bf16(dact[r, i] * u * s * (1 + g * (1 - s)))
+ *   dh[r, I + i] = bf16(dact[r, i] * g * s)
+ *   act[r, i]    = bf16(g * s * u)     (NULL: not written): moe_swiglu's result,
+ *                  for the weight gradient of the product behind it
+ * h, dh bf16 [R, 2I]; dact, act bf16 [R, I].  I % 8 == 0, pointers 16-byte aligned.
+ * dh may be the very buffer h, and act the very buffer dact.  R = 0 is a no-op.
+ * Errors: MOE_ERR_NULL, MOE_ERR_SHAPE, MOE_ERR_ALIGN, MOE_ERR_UNSUPPORTED
+ * (R*I/8 >= 2^31), MOE_ERR_HIP. */
+moe_status moe_swiglu_backward(const uint16_t* h, const uint16_t* dact, int32_t R, int32_t I, uint16_t* dh,
+                               uint16_t* act, void* stream);
+
+/* Of moe_combine, from dout, the gradient of its out:
+ *   dy[dest_of_src[t*k + j], :] = bf16(topk_weights[t, j] * dout[t, :])
+ *   dweights[t, j] = sum_c dout[t, c] * y[dest_of_src[t*k + j], c]     (fp32)
+ * Rows that dest_of_src does not name (padding) are neither read nor written.
+ * dout bf16 [T, H]; y, dy bf16 [rows, H]; topk_weights, dweights fp32 [T, k];
+ * dest_of_src as for moe_combine, no row twice.  dy may be the very buffer y.
+ * H % 8 == 0; bf16 pointers 16-byte aligned, the others 4-byte.  1 <= k <=
+ * MOE_K_MAX.  The same call gives the same bits every time.  T = 0 is a no-op.
+ * Errors: as moe_combine. */
+moe_status moe_combine_backward(const uint16_t* dout, const uint16_t* y, const float* topk_weights,
+                                const int32_t* dest_of_src, int32_t T, int32_t H, int32_t k, uint16_t* dy,
+                                float* dweights, void* stream);
+
+/* Of moe_expand_rows (dispatch):
+ *   dx[t, :] = bf16(residual[t, :] + sum_j dx_expanded[dest_of_src[t*k + j], :])
+ * in fp32 in j order, rounded once; residual NULL: none (with it, the gradient
+ * that x has from elsewhere: the skip connection, the router).  dx_expanded bf16
+ * [rows, H]; residual, dx bf16 [T, H]; dx may be the very buffer residual.
+ * Otherwise as moe_combine. */
+moe_status moe_expand_rows_backward(const uint16_t* dx_expanded, const int32_t* dest_of_src, const uint16_t* residual,
+                                    int32_t T, int32_t H, int32_t k, uint16_t* dx, void* stream);
+
+/* Of moe_route, from dweights, the gradient of its topk_weights: the selection
+ * passes none on, the softmax over the selected keys, in fp32,
+ *   ds_j = topk_weights[t, j] * (dweights[t, j] - sum_i topk_weights[t, i] dweights[t, i])
+ *   dlogits[t, topk_ids[t, j]] = ds_j, and 0 for every expert not selected
+ *   dbias[e] = sum_t dlogits[t, e]     (NULL: not written)
+ * topk_ids int32, topk_weights and dweights fp32 [T, k]; dlogits fp32 [T, E]; dbias
+ * fp32 [E]; all 4-byte aligned.  E, k and T*E as for moe_route.  Ids outside [0, E)
+ * are passed over.  T = 0 makes dbias zeros.  The same call gives the same bits
+ * every time.  Errors: MOE_ERR_NULL, MOE_ERR_SHAPE, MOE_ERR_ALIGN,
+ * MOE_ERR_UNSUPPORTED, MOE_ERR_HIP. */
+moe_status moe_route_backward(const int32_t* topk_ids, const float* topk_weights, const float* dweights, int32_t T,
+                              int32_t E, int32_t k, float* dlogits, float* dbias, void* stream);
 
 /* -------------------------------------------------------------- utilities */
 

@@ -20,6 +20,12 @@ Four calls, each a thin wrapper over the C ABI of the HIP library
     decode_layer(logits, k, x, w_gate_up, w_down)  the whole layer for T <= 64 tokens, experts included
     decode_layer_mxfp4(...)            the same on 4-bit (MXFP4) expert weights
     linear_mxfp4(x, w, scales)         product of T <= 64 tokens with MXFP4 weights
+    grouped_linear(x, w, offsets)      rows in expert order times their experts' weights, with bias, SwiGLU
+                                       and residual; without offsets a dense product
+    grouped_linear_mxfp8(...)          the same on MXFP8 rows and weights
+    grouped_linear_grad_x / _grad_w    gradients of that product to rows, weights and bias
+    swiglu_backward, combine_backward, expand_rows_backward, route_backward
+                                       gradients of the other steps
 
 Tensors are torch CUDA (HIP) tensors; bf16 tensors use torch.bfloat16.  Work
 is enqueued on torch's current stream and nothing synchronises.  Every call
@@ -28,7 +34,7 @@ can run the path without allocating.
 """
 from __future__ import annotations
 
-from ._binding import (DECODE_T_MAX, E_MAX, EXPORTED, K_MAX, LIB_PATH, NORM_H_MAX,  # noqa: F401
+from ._binding import (ACTS, DECODE_T_MAX, E_MAX, EXPORTED, K_MAX, LIB_PATH, NORM_H_MAX,  # noqa: F401
                        MoEGlueArgumentError, MoEGlueError, check, load)
 
 __all__ = ["route", "route_workspace_bytes", "alloc_route_outputs", "route_padded", "padded_rows", "expand_rows",
@@ -36,6 +42,8 @@ __all__ = ["route", "route_workspace_bytes", "alloc_route_outputs", "route_padde
            "route_expand", "route_expand_noalloc", "noalloc_scratch_bytes", "route_expand_padded", "route_expand_fp8", "route_expand_mxfp8", "swiglu", "combine",
            "rmsnorm", "rmsnorm_fp8", "rmsnorm_mxfp8", "decode_layer", "decode_layer_mxfp4",
            "decode_layer_workspace_bytes", "alloc_decode_outputs", "linear_mxfp4",
+           "grouped_linear", "grouped_linear_mxfp8", "grouped_linear_grad_x", "grouped_linear_grad_w",
+           "swiglu_backward", "combine_backward", "expand_rows_backward", "route_backward",
            "copy_probe", "mix_probe", "MoEGlueError", "MoEGlueArgumentError", "E_MAX", "K_MAX",
            "NORM_H_MAX", "DECODE_T_MAX"]
 
@@ -673,6 +681,254 @@ def linear_mxfp4(x, w, scales, out=None):
         _check_shape("out", out, torch.bfloat16, (T, N), x.device)
     _enqueue("moe_linear_mxfp4", x.device, x.data_ptr(), T, K, w.data_ptr(), scales.data_ptr(), N, out.data_ptr())
     return out
+
+
+def _group_args(w_shape, offsets, counts, device):
+    """Checks of the segments; returns E of weights of this shape (2-D: one expert has
+    all rows, and there are no segments)."""
+    torch = _torch()
+    if offsets is None:
+        if counts is not None:
+            raise MoEGlueArgumentError(1, "counts without offsets")
+        if len(w_shape) != 2:
+            raise MoEGlueArgumentError(2, f"without offsets the weights have 2 dims (got shape {list(w_shape)})")
+        return 1
+    if len(w_shape) != 3:
+        raise MoEGlueArgumentError(2, f"with offsets the weights have 3 dims (got shape {list(w_shape)})")
+    E = w_shape[0]
+    _check_shape("offsets", offsets, torch.int32, (E + 1,), device)
+    if counts is not None:
+        _check_shape("counts", counts, torch.int32, (E,), device)
+    return E
+
+
+def _grouped(fn, x, x_scales, w, w_scales, offsets, counts, bias, act, residual, out, pre):
+    torch = _torch()
+    bf16 = torch.bfloat16
+    mx = x_scales is not None
+    code = torch.uint8 if mx else bf16
+    _need_gpu("x", x, code, 2)
+    dev = x.device
+    R, K = x.shape
+    if w is None:
+        _need_gpu("w", w)
+    E = _group_args(w.shape, offsets, counts, dev)
+    N = w.shape[-2]
+    _check_shape("w", w, code, (*w.shape[:-1], K), dev)
+    if mx:
+        if K % 32 != 0:
+            raise MoEGlueArgumentError(2, f"K={K} is not a multiple of the 32-column block")
+        _check_shape("x_scales", x_scales, torch.uint8, (R, K // 32), dev)
+        _check_shape("w_scales", w_scales, torch.uint8, (*w.shape[:-1], K // 32), dev)
+    if act not in ACTS:
+        raise MoEGlueArgumentError(4, f"act={act!r} must be one of {list(ACTS)}")
+    swiglu = act == "swiglu"
+    if swiglu and N % 2:
+        raise MoEGlueArgumentError(2, f"w has an odd number of rows {N}; expected gate rows, then up rows")
+    shape = (R, N // 2 if swiglu else N)
+    if bias is not None:
+        _check_shape("bias", bias, bf16, tuple(w.shape[:-1]), dev)
+    if residual is not None:
+        _check_shape("residual", residual, bf16, shape, dev)
+    if pre is not None:
+        if not swiglu:
+            raise MoEGlueArgumentError(4, "pre without an activation")
+        _check_shape("pre", pre, bf16, (R, N), dev)
+    if out is None:
+        out = torch.empty(shape, dtype=bf16, device=dev)
+    else:
+        _check_shape("out", out, bf16, shape, dev)
+    rows = (_ptr(x), _ptr(x_scales)) if mx else (_ptr(x),)
+    weights = (_ptr(w), _ptr(w_scales)) if mx else (_ptr(w),)
+    _enqueue(fn, dev, *rows, R, _ptr(offsets), _ptr(counts), *weights, E, N, K, _ptr(bias), ACTS[act],
+             _ptr(residual), _ptr(pre), _ptr(out))
+    return out
+
+
+def grouped_linear(x, w, offsets=None, counts=None, bias=None, act=None, residual=None, out=None, pre=None):
+    """out = act(x w[e]^T + bias[e]) + residual for the rows of each expert's segment:
+    x bf16 [R, K], w bf16 [E, N, K], offsets int32 [E+1] (route()'s
+    "expert_offsets"), counts int32 [E] ("expert_counts", for padded segments),
+    bias bf16 [E, N]; act None or "swiglu" (w: gate rows, then up rows; out has N/2
+    columns); residual of out's shape, which may be `out` itself; pre bf16 [R, N],
+    with act, receives the product before it.  Without offsets w is [N, K] (bias
+    [N]) and all rows are its.  Rows of no segment of out and pre are left as they
+    are.  See moe_grouped_linear in include/moe_glue.h."""
+    return _grouped("moe_grouped_linear", x, None, w, None, offsets, counts, bias, act, residual, out, pre)
+
+
+def grouped_linear_mxfp8(x, x_scales, w, w_scales, offsets=None, counts=None, bias=None, act=None, residual=None,
+                         out=None, pre=None):
+    """grouped_linear() on MXFP8 rows and weights: E4M3 codes uint8 [R, K] and
+    [E, N, K], E8M0 scale bytes uint8 [R, K/32] and [E, N, K/32].  See
+    moe_grouped_linear_mxfp8 in include/moe_glue.h."""
+    if x_scales is None:
+        _need_gpu("x_scales", x_scales)
+    return _grouped("moe_grouped_linear_mxfp8", x, x_scales, w, w_scales, offsets, counts, bias, act, residual, out,
+                    pre)
+
+
+def grouped_linear_grad_x(dy, w, offsets=None, counts=None, out=None):
+    """dx = dy w[e] for the rows of each expert's segment: dy bf16 [R, N], w bf16
+    [E, N, K] ([N, K] without offsets); returns bf16 [R, K].  See
+    moe_grouped_linear_grad_x in include/moe_glue.h."""
+    torch = _torch()
+    _need_gpu("dy", dy, torch.bfloat16, 2)
+    dev = dy.device
+    R, N = dy.shape
+    if w is None:
+        _need_gpu("w", w)
+    E = _group_args(w.shape, offsets, counts, dev)
+    K = w.shape[-1]
+    _check_shape("w", w, torch.bfloat16, (*w.shape[:-2], N, K), dev)
+    if out is None:
+        out = torch.empty((R, K), dtype=torch.bfloat16, device=dev)
+    else:
+        _check_shape("out", out, torch.bfloat16, (R, K), dev)
+    _enqueue("moe_grouped_linear_grad_x", dev, _ptr(dy), R, _ptr(offsets), _ptr(counts), _ptr(w), E, N, K, _ptr(out))
+    return out
+
+
+def grouped_linear_grad_w(dy, x, offsets=None, counts=None, dtype=None, bias: bool = False, out=None, bias_out=None):
+    """dw[e] = dy^T x over each expert's rows, and with `bias` (or `bias_out`) the
+    column sums of dy: returns (dw [E, N, K] in `dtype`, bf16 (the default) or
+    fp32, dbias fp32 [E, N] or None); [N, K] and [N] without offsets.  See
+    moe_grouped_linear_grad_w in include/moe_glue.h."""
+    torch = _torch()
+    _need_gpu("dy", dy, torch.bfloat16, 2)
+    dev = dy.device
+    R, N = dy.shape
+    _need_gpu("x", x, torch.bfloat16, 2)
+    K = x.shape[1]
+    _check_shape("x", x, torch.bfloat16, (R, K), dev)
+    if offsets is None:
+        lead = ()
+    else:
+        _need_gpu("offsets", offsets, torch.int32, 1)
+        lead = (max(offsets.shape[0] - 1, 0),)
+    shape = (*lead, N, K)
+    E = _group_args(shape, offsets, counts, dev)
+    if dtype is None:
+        dtype = torch.bfloat16 if out is None else out.dtype
+    if dtype not in (torch.bfloat16, torch.float32):
+        raise MoEGlueArgumentError(4, f"dw must be bfloat16 or float32 (got {dtype})")
+    if out is None:
+        out = torch.empty(shape, dtype=dtype, device=dev)
+    else:
+        _check_shape("out", out, dtype, shape, dev)
+    if bias_out is not None:
+        _check_shape("bias_out", bias_out, torch.float32, (*lead, N), dev)
+    elif bias:
+        bias_out = torch.empty((*lead, N), dtype=torch.float32, device=dev)
+    _enqueue("moe_grouped_linear_grad_w", dev, _ptr(dy), _ptr(x), R, _ptr(offsets), _ptr(counts), E, N, K,
+             int(dtype == torch.float32), _ptr(out), _ptr(bias_out))
+    return out, bias_out
+
+
+def swiglu_backward(h, dact, out=None, act=None):
+    """The gradient of swiglu() to h, from dact, that of its result; returns dh
+    [R, 2I].  `act`: a bf16 [R, I] tensor that receives swiglu(h) as well.  See
+    moe_swiglu_backward in include/moe_glue.h."""
+    torch = _torch()
+    bf16 = torch.bfloat16
+    _need_gpu("h", h, bf16, 2)
+    R, I2 = h.shape
+    if I2 % 2:
+        raise MoEGlueArgumentError(2, f"h has an odd width {I2}; expected [R, 2I]")
+    I = I2 // 2
+    _check_shape("dact", dact, bf16, (R, I), h.device)
+    if out is None:
+        out = torch.empty_like(h)
+    else:
+        _check_shape("out", out, bf16, (R, I2), h.device)
+    if act is not None:
+        _check_shape("act", act, bf16, (R, I), h.device)
+    _enqueue("moe_swiglu_backward", h.device, _ptr(h), _ptr(dact), R, I, _ptr(out), _ptr(act))
+    return out
+
+
+def combine_backward(dout, y, topk_weights, dest_of_src, out=None, dweights=None):
+    """The gradients of combine(), from dout, that of its result; returns (dy of y's
+    shape, dweights fp32 [T, k]).  Rows of dy that dest_of_src does not name are
+    left as they are.  See moe_combine_backward in include/moe_glue.h."""
+    torch = _torch()
+    bf16 = torch.bfloat16
+    _need_gpu("dout", dout, bf16, 2)
+    dev = dout.device
+    T, H = dout.shape
+    _need_gpu("y", y, bf16, 2)
+    _check_shape("y", y, bf16, (y.shape[0], H), dev)
+    _need_gpu("topk_weights", topk_weights, torch.float32, 2)
+    k = topk_weights.shape[1]
+    _check_shape("topk_weights", topk_weights, torch.float32, (T, k), dev)
+    _check_shape("dest_of_src", dest_of_src, torch.int32, (T * k,), dev)
+    if y.shape[0] < T * k:
+        raise MoEGlueArgumentError(2, f"y has {y.shape[0]} rows, expected at least T*k={T * k}")
+    if out is None:
+        out = torch.empty_like(y)
+    else:
+        _check_shape("out", out, bf16, tuple(y.shape), dev)
+    if dweights is None:
+        dweights = torch.empty_like(topk_weights)
+    else:
+        _check_shape("dweights", dweights, torch.float32, (T, k), dev)
+    _enqueue("moe_combine_backward", dev, _ptr(dout), _ptr(y), _ptr(topk_weights), _ptr(dest_of_src), T, H, k,
+             _ptr(out), _ptr(dweights))
+    return out, dweights
+
+
+def expand_rows_backward(dx_expanded, dest_of_src, k: int, residual=None, out=None):
+    """The gradient of expand_rows(), from dx_expanded [rows, H], that of its result:
+    dx[t] = residual[t] + sum_j dx_expanded[dest_of_src[t*k+j]]; returns bf16
+    [T, H].  `residual` may be `out` itself.  See moe_expand_rows_backward in
+    include/moe_glue.h."""
+    torch = _torch()
+    bf16 = torch.bfloat16
+    _need_gpu("dx_expanded", dx_expanded, bf16, 2)
+    dev = dx_expanded.device
+    rows, H = dx_expanded.shape
+    _need_gpu("dest_of_src", dest_of_src, torch.int32, 1)
+    _same_device([("dest_of_src", dest_of_src)], dev)
+    if k < 1 or dest_of_src.numel() % k:
+        raise MoEGlueArgumentError(2, f"dest_of_src has {dest_of_src.numel()} entries, not a multiple of k={k}")
+    T = dest_of_src.numel() // k
+    if rows < T * k:
+        raise MoEGlueArgumentError(2, f"dx_expanded has {rows} rows, expected at least T*k={T * k}")
+    if residual is not None:
+        _check_shape("residual", residual, bf16, (T, H), dev)
+    if out is None:
+        out = torch.empty((T, H), dtype=bf16, device=dev)
+    else:
+        _check_shape("out", out, bf16, (T, H), dev)
+    _enqueue("moe_expand_rows_backward", dev, _ptr(dx_expanded), _ptr(dest_of_src), _ptr(residual), T, H, k,
+             _ptr(out))
+    return out
+
+
+def route_backward(topk_ids, topk_weights, dweights, E: int, bias: bool = False, out=None, bias_out=None):
+    """The gradient of route()'s weights to its logits, from dweights [T, k], and with
+    `bias` (or `bias_out`) to its bias; returns (dlogits fp32 [T, E], dbias fp32
+    [E] or None).  See moe_route_backward in include/moe_glue.h."""
+    torch = _torch()
+    f32 = torch.float32
+    _need_gpu("topk_weights", topk_weights, f32, 2)
+    dev = topk_weights.device
+    T, k = topk_weights.shape
+    _check_shape("topk_ids", topk_ids, torch.int32, (T, k), dev)
+    _check_shape("dweights", dweights, f32, (T, k), dev)
+    if not 0 < k <= min(E, K_MAX):
+        raise MoEGlueArgumentError(2, f"k={k} must be in [1, {min(E, K_MAX)}]")
+    if out is None:
+        out = torch.empty((T, E), dtype=f32, device=dev)
+    else:
+        _check_shape("out", out, f32, (T, E), dev)
+    if bias_out is not None:
+        _check_shape("bias_out", bias_out, f32, (E,), dev)
+    elif bias:
+        bias_out = torch.empty((E,), dtype=f32, device=dev)
+    _enqueue("moe_route_backward", dev, _ptr(topk_ids), _ptr(topk_weights), _ptr(dweights), T, E, k, _ptr(out),
+             _ptr(bias_out))
+    return out, bias_out
 
 
 def copy_probe(src, dst) -> None:

@@ -696,6 +696,179 @@ moe_status moe_linear_mxfp4(const uint16_t* x, int32_t T, int32_t K, const uint8
                     "moe_linear_mxfp4 launch");
 }
 
+}  // extern "C"
+
+namespace {
+
+moe_status check_k(const char* fn, int32_t T, int32_t k) {
+    if (k < 1 || k > MOE_K_MAX) return fail(MOE_ERR_SHAPE, "%s: k=%d must be in [1, %d]", fn, k, MOE_K_MAX);
+    if ((int64_t)T * k >= INT32_MAX) return fail(MOE_ERR_UNSUPPORTED, "%s: T*k too large", fn);
+    return MOE_OK;
+}
+
+// Segments, widths and tiles of the grouped products.
+moe_status check_grouped(const char* fn, const moe::GroupedRows& g, int32_t N, int32_t K, int64_t tiles) {
+    if (g.E < 1 || g.R < 0) return fail(MOE_ERR_SHAPE, "%s: E=%d must be >= 1 and R=%d >= 0", fn, g.E, g.R);
+    if (g.E > MOE_E_MAX) return fail(MOE_ERR_UNSUPPORTED, "%s: E=%d exceeds %d", fn, g.E, MOE_E_MAX);
+    if (g.offsets == nullptr && (g.E != 1 || g.counts != nullptr))
+        return fail(MOE_ERR_NULL, "%s: without expert_offsets there is one expert (E=%d) and no expert_counts", fn, g.E);
+    if (!aligned4(g.offsets) || !aligned4(g.counts))
+        return fail(MOE_ERR_ALIGN, "%s: offsets and counts must be 4-byte aligned", fn);
+    if (N > MOE_GROUPED_WIDTH_MAX || K > MOE_GROUPED_WIDTH_MAX)
+        return fail(MOE_ERR_UNSUPPORTED, "%s: N=%d or K=%d exceeds %d", fn, N, K, MOE_GROUPED_WIDTH_MAX);
+    if (tiles > MOE_GROUPED_TILES_MAX)
+        return fail(MOE_ERR_UNSUPPORTED, "%s: %lld tiles exceed %d", fn, (long long)tiles, MOE_GROUPED_TILES_MAX);
+    return MOE_OK;
+}
+
+moe_status check_grouped_width(const char* fn, const char* name, int32_t width, int32_t unit) {
+    if (width < 1) return fail(MOE_ERR_SHAPE, "%s: %s=%d must be >= 1", fn, name, width);
+    if (width % unit != 0)
+        return fail(unit == 32 ? MOE_ERR_SHAPE : MOE_ERR_ALIGN, "%s: %s=%d is not a multiple of %d", fn, name, width,
+                    unit);
+    return MOE_OK;
+}
+
+moe_status grouped_impl(const char* fn, const moe::GroupedArgs& g, bool mx, int act, void* stream) {
+    if (act != MOE_ACT_NONE && act != MOE_ACT_SWIGLU) return fail(MOE_ERR_UNSUPPORTED, "%s: act=%d", fn, act);
+    const bool swiglu = act == MOE_ACT_SWIGLU;
+    moe_status s = check_grouped_width(fn, "K", g.K, mx ? 32 : 8);
+    if (s == MOE_OK) s = check_grouped_width(fn, "N", g.N, swiglu ? 16 : 8);
+    if (s == MOE_OK) s = check_grouped(fn, g.rows, g.N, g.K, moe::grouped_linear_tiles(g.rows, g.N, swiglu));
+    if (s != MOE_OK) return s;
+    if (g.pre != nullptr && !swiglu) return fail(MOE_ERR_UNSUPPORTED, "%s: pre without an activation", fn);
+    if (g.rows.R == 0) return ok();
+    if (!g.x || !g.w || !g.out || (mx && (!g.xs || !g.ws))) return fail(MOE_ERR_NULL, "%s: NULL tensor pointer", fn);
+    if (!aligned16(g.x) || !aligned16(g.w) || !aligned16(g.bias) || !aligned16(g.residual) || !aligned16(g.pre) ||
+        !aligned16(g.out))
+        return fail(MOE_ERR_ALIGN, "%s: rows, weights, bias, residual and outputs must be 16-byte aligned", fn);
+    return from_hip(moe::launch_grouped_linear(g, swiglu, static_cast<hipStream_t>(stream)), fn);
+}
+
+}  // namespace
+
+extern "C" {
+
+moe_status moe_grouped_linear(const uint16_t* x, int32_t R, const int32_t* expert_offsets,
+                              const int32_t* expert_counts, const uint16_t* w, int32_t E, int32_t N, int32_t K,
+                              const uint16_t* bias, moe_act act, const uint16_t* residual, uint16_t* pre,
+                              uint16_t* out, void* stream) {
+    return grouped_impl("moe_grouped_linear",
+                        {{expert_offsets, expert_counts, E, R}, x, nullptr, w, nullptr, bias, residual, N, K, out, pre},
+                        false, act, stream);
+}
+
+moe_status moe_grouped_linear_mxfp8(const uint8_t* x, const uint8_t* x_scales, int32_t R,
+                                    const int32_t* expert_offsets, const int32_t* expert_counts, const uint8_t* w,
+                                    const uint8_t* w_scales, int32_t E, int32_t N, int32_t K, const uint16_t* bias,
+                                    moe_act act, const uint16_t* residual, uint16_t* pre, uint16_t* out,
+                                    void* stream) {
+    return grouped_impl(
+        "moe_grouped_linear_mxfp8",
+        {{expert_offsets, expert_counts, E, R}, x, x_scales, w, w_scales, bias, residual, N, K, out, pre}, true, act,
+        stream);
+}
+
+moe_status moe_grouped_linear_grad_x(const uint16_t* dy, int32_t R, const int32_t* expert_offsets,
+                                     const int32_t* expert_counts, const uint16_t* w, int32_t E, int32_t N, int32_t K,
+                                     uint16_t* dx, void* stream) {
+    const char* fn = "moe_grouped_linear_grad_x";
+    const moe::GroupedRows rows = {expert_offsets, expert_counts, E, R};
+    moe_status s = check_grouped_width(fn, "K", K, 8);
+    if (s == MOE_OK) s = check_grouped_width(fn, "N", N, 8);
+    if (s == MOE_OK) s = check_grouped(fn, rows, N, K, moe::grouped_linear_tiles(rows, K, false));
+    if (s != MOE_OK) return s;
+    if (R == 0) return ok();
+    if (!dy || !w || !dx) return fail(MOE_ERR_NULL, "%s: NULL tensor pointer", fn);
+    if (!aligned16(dy) || !aligned16(w) || !aligned16(dx))
+        return fail(MOE_ERR_ALIGN, "%s: bf16 tensors must be 16-byte aligned", fn);
+    // the sum runs over w's rows: its N rows of K columns are the product's K rows of N
+    return from_hip(moe::launch_grouped_grad_x({rows, dy, nullptr, w, nullptr, nullptr, nullptr, K, N, dx, nullptr},
+                                               static_cast<hipStream_t>(stream)),
+                    fn);
+}
+
+moe_status moe_grouped_linear_grad_w(const uint16_t* dy, const uint16_t* x, int32_t R, const int32_t* expert_offsets,
+                                     const int32_t* expert_counts, int32_t E, int32_t N, int32_t K, int32_t dw_fp32,
+                                     void* dw, float* dbias, void* stream) {
+    const char* fn = "moe_grouped_linear_grad_w";
+    const moe::GroupedRows rows = {expert_offsets, expert_counts, E, R};
+    moe_status s = check_grouped_width(fn, "K", K, 8);
+    if (s == MOE_OK) s = check_grouped_width(fn, "N", N, 8);
+    if (s == MOE_OK) s = check_grouped(fn, rows, N, K, moe::grouped_grad_w_tiles(E, N, K));
+    if (s != MOE_OK) return s;
+    if (!dw || (R > 0 && (!dy || !x))) return fail(MOE_ERR_NULL, "%s: NULL tensor pointer", fn);
+    if (!aligned16(dy) || !aligned16(x) || !aligned16(dw))
+        return fail(MOE_ERR_ALIGN, "%s: dy, x and dw must be 16-byte aligned", fn);
+    if (!aligned4(dbias)) return fail(MOE_ERR_ALIGN, "%s: dbias must be 4-byte aligned", fn);
+    return from_hip(moe::launch_grouped_grad_w({rows, dy, x, N, K, dw, dw_fp32 != 0, dbias},
+                                               static_cast<hipStream_t>(stream)),
+                    fn);
+}
+
+moe_status moe_swiglu_backward(const uint16_t* h, const uint16_t* dact, int32_t R, int32_t I, uint16_t* dh,
+                               uint16_t* act, void* stream) {
+    const char* fn = "moe_swiglu_backward";
+    const moe_status s = check_rows(fn, R, I, "I");
+    if (s != MOE_OK) return s;
+    if (R == 0) return ok();
+    if (!h || !dact || !dh) return fail(MOE_ERR_NULL, "%s: NULL tensor pointer", fn);
+    if (!aligned16(h) || !aligned16(dact) || !aligned16(dh) || !aligned16(act))
+        return fail(MOE_ERR_ALIGN, "%s: pointers must be 16-byte aligned", fn);
+    return from_hip(moe::launch_swiglu_backward(h, dact, R, I, dh, act, static_cast<hipStream_t>(stream)), fn);
+}
+
+moe_status moe_combine_backward(const uint16_t* dout, const uint16_t* y, const float* topk_weights,
+                                const int32_t* dest_of_src, int32_t T, int32_t H, int32_t k, uint16_t* dy,
+                                float* dweights, void* stream) {
+    const char* fn = "moe_combine_backward";
+    moe_status s = check_rows(fn, T, H, "H");
+    if (s == MOE_OK) s = check_k(fn, T, k);
+    if (s != MOE_OK) return s;
+    if (T == 0) return ok();
+    if (!dout || !y || !topk_weights || !dest_of_src || !dy || !dweights)
+        return fail(MOE_ERR_NULL, "%s: NULL tensor pointer", fn);
+    if (!aligned16(dout) || !aligned16(y) || !aligned16(dy))
+        return fail(MOE_ERR_ALIGN, "%s: dout, y and dy must be 16-byte aligned", fn);
+    if (!aligned4(topk_weights) || !aligned4(dest_of_src) || !aligned4(dweights))
+        return fail(MOE_ERR_ALIGN, "%s: weights, their gradient and dest_of_src must be 4-byte aligned", fn);
+    return from_hip(moe::launch_combine_backward(dout, y, topk_weights, dest_of_src, T, H, k, dy, dweights,
+                                                 static_cast<hipStream_t>(stream)),
+                    fn);
+}
+
+moe_status moe_expand_rows_backward(const uint16_t* dx_expanded, const int32_t* dest_of_src, const uint16_t* residual,
+                                    int32_t T, int32_t H, int32_t k, uint16_t* dx, void* stream) {
+    const char* fn = "moe_expand_rows_backward";
+    moe_status s = check_rows(fn, T, H, "H");
+    if (s == MOE_OK) s = check_k(fn, T, k);
+    if (s != MOE_OK) return s;
+    if (T == 0) return ok();
+    if (!dx_expanded || !dest_of_src || !dx) return fail(MOE_ERR_NULL, "%s: NULL tensor pointer", fn);
+    if (!aligned16(dx_expanded) || !aligned16(residual) || !aligned16(dx))
+        return fail(MOE_ERR_ALIGN, "%s: bf16 tensors must be 16-byte aligned", fn);
+    if (!aligned4(dest_of_src)) return fail(MOE_ERR_ALIGN, "%s: dest_of_src must be 4-byte aligned", fn);
+    return from_hip(moe::launch_expand_backward(dx_expanded, dest_of_src, residual, T, H, k, dx,
+                                                static_cast<hipStream_t>(stream)),
+                    fn);
+}
+
+moe_status moe_route_backward(const int32_t* topk_ids, const float* topk_weights, const float* dweights, int32_t T,
+                              int32_t E, int32_t k, float* dlogits, float* dbias, void* stream) {
+    const char* fn = "moe_route_backward";
+    const moe_status s = check_route_sizes(T, E, k);
+    if (s != MOE_OK) return s;
+    if (T > 0 && (!topk_ids || !topk_weights || !dweights || !dlogits))
+        return fail(MOE_ERR_NULL, "%s: NULL tensor pointer", fn);
+    if (!aligned4(topk_ids) || !aligned4(topk_weights) || !aligned4(dweights) || !aligned4(dlogits) ||
+        !aligned4(dbias))
+        return fail(MOE_ERR_ALIGN, "%s: pointers must be 4-byte aligned", fn);
+    if (T == 0 && dbias == nullptr) return ok();
+    return from_hip(moe::launch_route_backward(topk_ids, topk_weights, dweights, T, E, k, dlogits, dbias,
+                                               static_cast<hipStream_t>(stream)),
+                    fn);
+}
+
 int moe_testing_force(int route_variant, int expand_order, int workgroups_per_group) {
     if (route_variant < 0 || route_variant > 3 || expand_order < 0 || expand_order > 4 || workgroups_per_group < 0 ||
         workgroups_per_group > 4096)

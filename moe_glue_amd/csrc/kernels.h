@@ -260,6 +260,58 @@ hipError_t launch_decode_layer(const DecodeLayerArgs& a, hipStream_t stream);
 hipError_t launch_linear_mxfp4(const void* x, int T, int K, const uint8_t* w, const uint8_t* scales, int N, void* y,
                                hipStream_t stream);
 
+// -------------------------------------------- experts' products and gradients
+constexpr int kGroupedRows = 256;  // rows of a whole tile
+struct GroupedRows {
+    const int32_t* offsets;  // [E+1] on the device, or null: one expert has all R rows
+    const int32_t* counts;   // [E], or null: a segment ends where the next begins
+    int E, R;
+};
+// Workgroups that any E segments of R rows take: one per row tile and column tile.
+inline int64_t grouped_tiles(const GroupedRows& g, int col_tiles) {
+    const int64_t partial = g.E < g.R ? g.E : g.R;
+    return (g.offsets == nullptr ? (g.R + kGroupedRows - 1) / kGroupedRows : g.R / kGroupedRows + partial) *
+           (int64_t)col_tiles;
+}
+// out = act(x w_e^T + bias_e) + residual; as grad_x: out = x w_e, x being dy and w [K, N].
+struct GroupedArgs {
+    GroupedRows rows;
+    const void* x;            // bf16 [R, K], or E4M3 codes
+    const uint8_t* xs;        // E8M0 [R, K/32], or null (bf16)
+    const void* w;            // [E, N, K] ([E, K, N] as grad_x)
+    const uint8_t* ws;        // E8M0 [E, N, K/32]
+    const uint16_t* bias;     // bf16 [E, N] or null
+    const uint16_t* residual; // bf16 [R, out columns] or null
+    int N, K;
+    uint16_t* out;            // bf16 [R, N], or [R, N/2] behind SwiGLU
+    uint16_t* pre;            // bf16 [R, N] or null: the rows before SwiGLU
+};
+int64_t grouped_linear_tiles(const GroupedRows& rows, int cols, bool swiglu);
+hipError_t launch_grouped_linear(const GroupedArgs& g, bool swiglu, hipStream_t stream);
+hipError_t launch_grouped_grad_x(const GroupedArgs& g, hipStream_t stream);
+struct GroupedGradArgs {
+    GroupedRows rows;
+    const uint16_t* dy;  // bf16 [R, N]
+    const uint16_t* x;   // bf16 [R, K]
+    int N, K;
+    void* dw;            // bf16 or fp32 [E, N, K]
+    bool wide;           // dw in fp32
+    float* db;           // fp32 [E, N] or null
+};
+int64_t grouped_grad_w_tiles(int E, int N, int K);
+hipError_t launch_grouped_grad_w(const GroupedGradArgs& g, hipStream_t stream);
+
+// ------------------------------------------- gradients of the streaming steps
+hipError_t launch_swiglu_backward(const void* h, const void* dact, int R, int I, void* dh, void* act,
+                                  hipStream_t stream);
+hipError_t launch_combine_backward(const void* dout, const void* y, const float* topk_weights,
+                                   const int32_t* dest_of_src, int T, int H, int k, void* dy, float* dweights,
+                                   hipStream_t stream);
+hipError_t launch_expand_backward(const void* dx_expanded, const int32_t* dest_of_src, const void* residual, int T,
+                                  int H, int k, void* dx, hipStream_t stream);
+hipError_t launch_route_backward(const int32_t* topk_ids, const float* topk_weights, const float* dweights, int T,
+                                 int E, int k, float* dlogits, float* dbias, hipStream_t stream);
+
 // ------------------------------------------------------- built-in scratch
 // Bytes of the file-scope device array behind moe_route_expand_noalloc.
 constexpr size_t kNoAllocScratchBytes = (size_t)MOE_NOALLOC_SCRATCH_BYTES;
