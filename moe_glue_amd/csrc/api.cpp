@@ -734,7 +734,7 @@ moe_status grouped_impl(const char* fn, const moe::GroupedArgs& g, bool mx, int 
     const bool swiglu = act == MOE_ACT_SWIGLU;
     moe_status s = check_grouped_width(fn, "K", g.K, mx ? 32 : 8);
     if (s == MOE_OK) s = check_grouped_width(fn, "N", g.N, swiglu ? 16 : 8);
-    if (s == MOE_OK) s = check_grouped(fn, g.rows, g.N, g.K, moe::grouped_linear_tiles(g.rows, g.N, swiglu));
+    if (s == MOE_OK) s = check_grouped(fn, g.rows, g.N, g.K, moe::grouped_linear_tiles(g.rows, g.N));
     if (s != MOE_OK) return s;
     if (g.pre != nullptr && !swiglu) return fail(MOE_ERR_UNSUPPORTED, "%s: pre without an activation", fn);
     if (g.rows.R == 0) return ok();
@@ -754,7 +754,8 @@ moe_status moe_grouped_linear(const uint16_t* x, int32_t R, const int32_t* exper
                               const uint16_t* bias, moe_act act, const uint16_t* residual, uint16_t* pre,
                               uint16_t* out, void* stream) {
     return grouped_impl("moe_grouped_linear",
-                        {{expert_offsets, expert_counts, E, R}, x, nullptr, w, nullptr, bias, residual, N, K, out, pre},
+                        {{expert_offsets, expert_counts, E, R}, x, nullptr, w, nullptr, bias, residual, N, K, out, pre,
+                         false},
                         false, act, stream);
 }
 
@@ -765,8 +766,9 @@ moe_status moe_grouped_linear_mxfp8(const uint8_t* x, const uint8_t* x_scales, i
                                     void* stream) {
     return grouped_impl(
         "moe_grouped_linear_mxfp8",
-        {{expert_offsets, expert_counts, E, R}, x, x_scales, w, w_scales, bias, residual, N, K, out, pre}, true, act,
-        stream);
+        {{expert_offsets, expert_counts, E, R}, x, x_scales, w, w_scales, bias, residual, N, K, out, pre,
+         K % 128 == 0 && aligned4(x_scales) && aligned4(w_scales)},
+        true, act, stream);
 }
 
 moe_status moe_grouped_linear_grad_x(const uint16_t* dy, int32_t R, const int32_t* expert_offsets,
@@ -776,14 +778,14 @@ moe_status moe_grouped_linear_grad_x(const uint16_t* dy, int32_t R, const int32_
     const moe::GroupedRows rows = {expert_offsets, expert_counts, E, R};
     moe_status s = check_grouped_width(fn, "K", K, 8);
     if (s == MOE_OK) s = check_grouped_width(fn, "N", N, 8);
-    if (s == MOE_OK) s = check_grouped(fn, rows, N, K, moe::grouped_linear_tiles(rows, K, false));
+    if (s == MOE_OK) s = check_grouped(fn, rows, N, K, moe::grouped_linear_tiles(rows, K));
     if (s != MOE_OK) return s;
     if (R == 0) return ok();
     if (!dy || !w || !dx) return fail(MOE_ERR_NULL, "%s: NULL tensor pointer", fn);
     if (!aligned16(dy) || !aligned16(w) || !aligned16(dx))
         return fail(MOE_ERR_ALIGN, "%s: bf16 tensors must be 16-byte aligned", fn);
     // the sum runs over w's rows: its N rows of K columns are the product's K rows of N
-    return from_hip(moe::launch_grouped_grad_x({rows, dy, nullptr, w, nullptr, nullptr, nullptr, K, N, dx, nullptr},
+    return from_hip(moe::launch_grouped_grad_x({rows, dy, nullptr, w, nullptr, nullptr, nullptr, K, N, dx, nullptr, false},
                                                static_cast<hipStream_t>(stream)),
                     fn);
 }

@@ -2,15 +2,14 @@
 // gradients: the tile that the kernels of grouped_linear.hip and
 // grouped_grad.hip share.
 //
-// A workgroup of eight waves computes D = A B^T over a tile of 32 MT rows (m) by
-// 64 NT columns (n), fp32, with v_mfma_f32_16x16x32_bf16 (or the block-scaled
-// 16x16x128 on MXFP8).  Steps of 128 bytes of a row (64 bf16 or 128 E4M3) of both
-// operands go from memory to LDS without registers (buffer_load_dwordx4 .. lds,
-// 16 bytes a lane), through a ring of as many stages as LDS holds: loads of a
-// stage are in flight while the stages before it are multiplied, with one barrier
-// a step.  An operand lies in memory with the summed index along its rows
-// ("rows": x, dy for dx, the weights of the forward product) or across them
-// ("columns": the weights for dx, both operands of the weight gradient).
+// A workgroup of eight waves, two by four, computes D = A B^T over a tile of 64 MH
+// rows (m) by 256 columns (n) in fp32, with v_mfma_f32_16x16x32_bf16 (or the
+// block-scaled 16x16x128 on MXFP8).  Steps of 128 bytes of a row (64 bf16 or 128
+// E4M3) of both operands go from memory to LDS without registers
+// (buffer_load_dwordx4 .. lds, 16 bytes a lane), two to four steps ahead.  An
+// operand lies in memory with the summed index along its rows ("rows": x, dy for dx,
+// the weights of the forward product) or across them ("columns": the weights for dx,
+// both operands of the weight gradient).
 //
 //   rows     LDS rows of 128 bytes; lane l of a fragment reads 16-byte pieces
 //            l / 16 and 4 + l / 16 of row l % 16: k 8 (l / 16) .. + 7 of each half
@@ -27,6 +26,8 @@
 // 16-lane rows between two tiles makes them eight: 16-byte stores in bf16.
 #pragma once
 
+#include <type_traits>
+
 #include "device_common.h"
 #include "kernels.h"
 
@@ -34,6 +35,7 @@ namespace moe {
 
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef short s16x4 __attribute__((ext_vector_type(4)));
+typedef short s16x8 __attribute__((ext_vector_type(8)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef int i32x4 __attribute__((ext_vector_type(4)));
 typedef int i32x8 __attribute__((ext_vector_type(8)));
@@ -57,66 +59,53 @@ __device__ __forceinline__ Segment segment(const GroupedRows& g, int e) {
     return {first, min(max(n, 0), g.R - first)};
 }
 
-// Row tiles of an expert with n rows: up to kSplitTiles tiles share the rows
-// evenly (in 32s), more are full but for the last.
-constexpr int kSplitTiles = 4;
-__host__ __device__ __forceinline__ int row_tiles(int n) { return (n + kGroupedRows - 1) / kGroupedRows; }
-__host__ __device__ __forceinline__ int tile_rows(int n) {
-    const int t = row_tiles(n);
-    return t > kSplitTiles || t == 0 ? kGroupedRows : ((n + t - 1) / t + 31) / 32 * 32;
-}
+// Row tiles of an expert with n rows, each of up to `whole` (a multiple of 64): n
+// in units of 64 rows, dealt out evenly.
+__host__ __device__ __forceinline__ int row_tiles(int n, int whole) { return (n + whole - 1) / whole; }
 
 struct Tile {
-    int e;      // expert, -1: none
+    int e;      // expert
     int first;  // first row
-    int rows;
-    int last_rows;  // rows of a whole tile of this expert (what the tile is laid out for)
+    int rows;   // 0: no tile
     int col;    // column tile
 };
 
 // The tile of this workgroup.  Tiles are numbered expert by expert; in an expert,
 // groups of kTogether row tiles by column tile by row tile.  Each XCD (workgroups
 // b with equal b % 8) takes one run of them, so that the weights that row tiles
-// share, and the rows that column tiles share, meet in its L2.  Every wave does
-// this on its own: a lane sums the tiles of up to 8 experts, the wave's prefix
-// sums find the one that holds the tile.
+// share, and the rows that column tiles share, meet in its L2.  Every wave looks for
+// itself: a lane sums the tiles of up to 8 experts and the wave's prefix sums find the
+// lane that holds the tile; then its experts, one a lane, the same way.
 constexpr int kTogether = 8;
-__device__ __forceinline__ Tile find_tile(const GroupedRows& g, int col_tiles) {
+__device__ __forceinline__ Tile find_tile(const GroupedRows& g, int col_tiles, int whole) {
     const int lane = (int)(threadIdx.x % kWave);
     const int per = (g.E + kWave - 1) / kWave;
     int mine = 0;
     for (int i = 0; i < per; ++i) {
         const int e = lane * per + i;
-        if (e < g.E) mine += row_tiles(segment(g, e).n);
+        if (e < g.E) mine += row_tiles(segment(g, e).n, whole);
     }
     const int upto = wave_inclusive_sum(mine);
     const int total = __builtin_amdgcn_readlane(upto, kWave - 1) * col_tiles;
     const int run = (total + 7) / 8;
     const int u = (int)(blockIdx.x % 8) * run + (int)(blockIdx.x / 8);
-    Tile t = {-1, 0, 0, 0, 0};
-    if ((int)(blockIdx.x / 8) >= run || u >= total) return t;
+    if ((int)(blockIdx.x / 8) >= run || u >= total) return {0, 0, 0, 0};
     const int owner = __builtin_ctzll(__ballot(upto * col_tiles > u));
-    int before = __builtin_amdgcn_readlane(upto - mine, owner);
-    for (int i = 0; i < per; ++i) {
-        const int e = owner * per + i;
-        const Segment s = segment(g, e);
-        const int tiles = row_tiles(s.n);
-        if (u < (before + tiles) * col_tiles) {
-            const int v = u - before * col_tiles;
-            const int group = v / (kTogether * col_tiles);
-            const int in_group = min(kTogether, tiles - group * kTogether);
-            const int at = v - group * kTogether * col_tiles;
-            const int m = group * kTogether + at % in_group;
-            t.e = e;
-            t.last_rows = tile_rows(s.n);
-            t.first = s.first + m * t.last_rows;
-            t.rows = min(t.last_rows, s.n - m * t.last_rows);
-            t.col = at / in_group;
-            return t;
-        }
-        before += tiles;
-    }
-    return t;
+    const int before = __builtin_amdgcn_readlane(upto - mine, owner);
+    Segment s = {0, 0};
+    if (lane < per && owner * per + lane < g.E) s = segment(g, owner * per + lane);
+    const int here = row_tiles(s.n, whole), until = before + wave_inclusive_sum(here);
+    const int which = __builtin_ctzll(__ballot(until * col_tiles > u));
+    const int n = __builtin_amdgcn_readlane(s.n, which), tiles = __builtin_amdgcn_readlane(here, which);
+    const int v = u - __builtin_amdgcn_readlane(until - here, which) * col_tiles;
+    const int group = v / (kTogether * col_tiles);
+    const int in_group = min(kTogether, tiles - group * kTogether);
+    const int at = v - group * kTogether * col_tiles;
+    const int m = group * kTogether + at % in_group;
+    const int units = (n + 63) / 64, each = units / tiles, more = units % tiles;
+    const int first = (m * each + min(m, more)) * 64;
+    return {owner * per + which, __builtin_amdgcn_readlane(s.first, which) + first,
+            min((each + (m < more ? 1 : 0)) * 64, n - first), at / in_group};
 }
 
 // ------------------------------------------------------------------- loads
@@ -128,31 +117,34 @@ __device__ __forceinline__ void load_to_lds(__amdgpu_buffer_rsrc_t r, uint32_t l
     __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (MOE_LDS void*)lds, 16, (int)lane, (int)scalar, 0, 0);
 }
 
-// An operand with the summed index along its rows: `rows` rows of `ld` bytes from
-// base on; J * 64 rows of LDS, J loads a wave.  Rows past the last read zeros, as
-// do bytes past a row's end.
+// An operand with the summed index along its rows, of `ld` bytes each; load j of a
+// wave brings eight of 64 LDS rows.  Rows past the end of their buffer and bytes past
+// a row's end read zeros.
 template <int J>
 struct RowsOperand {
-    static constexpr int LDS_BYTES = J * 64 * kStepBytes;
-    __amdgpu_buffer_rsrc_t buf;
     uint32_t at[J];
     uint32_t piece, ld;
-    __device__ __forceinline__ void set(const uint8_t* base, int64_t bytes, uint32_t ld_, uint32_t first_row,
-                                        uint32_t row_step) {
+    __device__ __forceinline__ void set(uint32_t ld_) {
         const uint32_t lane = threadIdx.x % kWave, wave = uniform(threadIdx.x / kWave);
-        buf = grouped_buffer(base, bytes);
         ld = ld_;
-        const uint32_t row = wave * 8 + lane / 8;  // of LDS, modulo 64
+        const uint32_t row = wave * 8 + lane / 8;
         piece = (lane % 8 ^ (row / 2 % 8)) * 16;
 #pragma unroll
-        for (int j = 0; j < J; ++j) at[j] = (first_row + lane / 8 + j * row_step) * ld + piece;
+        for (int j = 0; j < J; ++j) at[j] = (row + j * 64) * ld + piece;
     }
-    __device__ __forceinline__ void load(int step, uint8_t* lds) const {
+    // Loads FROM .. TO - 1 of a step, the first of them to LDS row 0.  Steps in order:
+    // from the one that holds a row's end on, lanes past it stay turned away.
+    template <int FROM, int TO>
+    __device__ __forceinline__ void load(__amdgpu_buffer_rsrc_t buf, int step, uint8_t* lds) {
         const uint32_t wave = uniform(threadIdx.x / kWave);
         const uint32_t k = (uint32_t)step * kStepBytes;
-        const bool past = k + piece >= ld;
+        if (k + kStepBytes > ld) {
+            const bool past = k + piece >= ld;
 #pragma unroll
-        for (int j = 0; j < J; ++j) load_to_lds(buf, past ? kPastEnd : at[j], k, lds + (j * 8 + wave) * 1024);
+            for (int j = FROM; j < TO; ++j) at[j] = past ? kPastEnd : at[j];
+        }
+#pragma unroll
+        for (int j = FROM; j < TO; ++j) load_to_lds(buf, at[j], k, lds + ((j - FROM) * 8 + wave) * 1024);
     }
 };
 
@@ -181,7 +173,7 @@ struct ColumnsOperand {
             at[j] = row * ld + ((piece / 2 ^ key) * 2 + piece % 2) * 16;
         }
     }
-    __device__ __forceinline__ void load(int step, uint8_t* lds) const {
+    __device__ __forceinline__ void load(int step, uint8_t* lds) {
         const uint32_t wave = uniform(threadIdx.x / kWave);
         const int64_t from = (int64_t)step * 64 * ld;
         const __amdgpu_buffer_rsrc_t buf = grouped_buffer(base + from, bytes - from);
@@ -191,34 +183,128 @@ struct ColumnsOperand {
 };
 
 // --------------------------------------------------------------- fragments
-// 16 bytes of row r, piece c (0..7) of a rows operand in LDS.
-__device__ __forceinline__ uint32_t rows_at(uint32_t row, uint32_t piece) {
-    return row * kStepBytes + ((piece ^ (row / 2 % 8)) * 16);
-}
-// A lane's place in a columns operand of W bytes a row, less its unit of 16
-// columns: add the step half's 32 W, then xor unit * 32.
-template <int W>
-__device__ __forceinline__ uint32_t columns_at() {
-    const uint32_t lane = threadIdx.x % kWave;
-    const uint32_t row = lane / 16 * 8 + lane % 16 / 4;
-    const uint32_t key = row % 4 + row / 8 % 2 * 4;
-    return row * W + key * 32 + lane % 4 * 8;
-}
-template <int W>
-__device__ __forceinline__ bf16x8 columns_fragment(const uint8_t* lds, uint32_t at) {
-    const s16x4 a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((MOE_LDS s16x4*)(lds + at));
-    const s16x4 b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((MOE_LDS s16x4*)(lds + at + 4 * W));
-    typedef short s16x8 __attribute__((ext_vector_type(8)));
-    return __builtin_bit_cast(bf16x8, s16x8{a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]});
+// 16 rows (columns of D) by a step's k, in a lane's registers.
+struct RowsFragment {
+    i32x4 lo, hi;
+    // The lane's place for the 16 rows from row 0 on; 16 rows further is 2048 bytes on.
+    static __device__ __forceinline__ uint32_t at() {
+        const uint32_t lane = threadIdx.x % kWave, row = lane % 16;
+        return row * kStepBytes + (lane / 16 ^ row / 2) * 16;
+    }
+    __device__ __forceinline__ void read(const uint8_t* p, uint32_t at) {
+        lo = *reinterpret_cast<const i32x4*>(p + at);
+        hi = *reinterpret_cast<const i32x4*>(p + (at ^ 64));
+    }
+    template <int H>
+    __device__ __forceinline__ bf16x8 half() const {
+        return __builtin_bit_cast(bf16x8, H == 0 ? lo : hi);
+    }
+    __device__ __forceinline__ i32x8 whole() const { return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7); }
+};
+template <int W>  // bytes of an LDS row
+struct ColumnsFragment {
+    s16x4 v[4];
+    // The lane's place for unit 0: xor the unit's 32 bytes in.
+    static __device__ __forceinline__ uint32_t at() {
+        const uint32_t lane = threadIdx.x % kWave;
+        const uint32_t row = lane / 16 * 8 + lane % 16 / 4;
+        return row * W + (row % 4 + row / 8 % 2 * 4) * 32 + lane % 4 * 8;
+    }
+    __device__ __forceinline__ void read(const uint8_t* p, uint32_t at) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)  // k 0..3, 4..7 of the lane's eight, of either 32
+            v[i] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((MOE_LDS s16x4*)(p + at + (i / 2 * 32 + i % 2 * 4) * W));
+    }
+    template <int H>
+    __device__ __forceinline__ bf16x8 half() const {
+        return __builtin_bit_cast(bf16x8, __builtin_shufflevector(v[2 * H], v[2 * H + 1], 0, 1, 2, 3, 4, 5, 6, 7));
+    }
+};
+
+template <int N, class F>
+__device__ __forceinline__ void unrolled(F&& f) {
+    if constexpr (N > 0) {
+        unrolled<N - 1>(f);
+        f(std::integral_constant<int, N - 1>{});
+    }
 }
 
-// Waits until at most N of this wave's loads are in flight and its LDS reads are
-// done, then for the other waves.
-template <int N>
-__device__ __forceinline__ void wait_and_meet() {
-    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(N) : "memory");
+// ------------------------------------------------------------------- steps
+__device__ __forceinline__ void meet() {
+    asm volatile("" ::: "memory");
     __builtin_amdgcn_s_barrier();
     asm volatile("" ::: "memory");
+}
+__device__ __forceinline__ void reads_done() { asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory"); }
+// At most N of this wave's loads in flight.
+template <int N>
+__device__ __forceinline__ void loads_done() {
+    asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
+}
+
+// The steps of a tile.  A step is four quarters: the halves of the wave's rows by the
+// halves of its columns,
+//   0: rows 0, columns 0   1: rows 0, columns 1   2: rows 1, columns 1   3: rows 1, columns 0
+// each of them a part that fills registers from LDS (and asks for the step after next)
+// and a part of matrix instructions, with a barrier behind either.  The second four
+// waves start one barrier late: on each SIMD one wave multiplies while the other reads.
+//   read_a(h, buffer), read_b(h, buffer)   half h of a step to registers
+//   multiply(ha, hb)
+//   load(q, step, buffer)                  what quarter q = 1, 2, 3 asks for
+// There are two buffers, and a part of one is asked for again as soon as both halves of
+// the waves have read it: rows 0 and columns 0 in quarter 1, columns 1 in quarter 2,
+// rows 1 in quarter 3, L1, L2 and L3 loads of a wave.  So everything is asked for a step
+// and a half before it is read, and each wait leaves the loads of a step and more in
+// flight.  LEFT0: how many of quarter 3's loads (or 2's and 3's) the first quarter does
+// not need; LEFT1: the second; the third needs all.
+template <int L1, int L2, int L3, int LEFT0, int LEFT1, class ReadA, class ReadB, class Multiply, class Load>
+__device__ __forceinline__ void run_steps(int steps, const ReadA& read_a, const ReadB& read_b,
+                                          const Multiply& multiply, const Load& load) {
+    constexpr std::integral_constant<int, 0> q0{};
+    constexpr std::integral_constant<int, 1> q1{};
+    constexpr std::integral_constant<int, 2> q2{};
+    constexpr std::integral_constant<int, 3> q3{};
+    constexpr int STEP = L1 + L2 + L3;
+    const bool late = uniform(threadIdx.x / kWave) >= 4;
+    if (steps == 0) return;
+#pragma unroll
+    for (int s = 0; s < 2; ++s) {
+        load(q1, s, s);
+        load(q2, s, s);
+        load(q3, s, s);
+    }
+    loads_done<LEFT0 + STEP>();
+    meet();
+    if (late) meet();
+    const auto quarter = [&](auto ha, auto hb) {
+        meet();
+        __builtin_amdgcn_s_setprio(1);
+        multiply(ha, hb);
+        __builtin_amdgcn_s_setprio(0);
+        meet();
+    };
+    for (int step = 0; step < steps; ++step) {
+        const int buf = step % 2;
+        read_a(q0, buf);
+        read_b(q0, buf);
+        loads_done<LEFT1 + STEP>();
+        reads_done();
+        quarter(q0, q0);
+        read_b(q1, buf);
+        load(q1, step + 2, buf);
+        loads_done<STEP + L1>();
+        reads_done();
+        quarter(q0, q1);
+        read_a(q1, buf);
+        load(q2, step + 2, buf);
+        reads_done();
+        quarter(q1, q1);
+        load(q3, step + 2, buf);
+        loads_done<LEFT0 + STEP>();
+        quarter(q1, q0);
+    }
+    if (!late) meet();
+    loads_done<0>();  // none may land in the next workgroup's LDS
 }
 
 // Eight neighbouring columns of one row of D, of the tile pair (a, b): see

@@ -55,34 +55,39 @@ __global__ __launch_bounds__(kGroupedThreads, 4) void grad_w_kernel(GroupedGradA
     }
     const bool sum_here = DB && k0 == 0 && wn == 0;
     constexpr int AW = ColumnsOperand<AJ>::W, BW = ColumnsOperand<NT>::W;
-    const uint32_t a_at = columns_at<AW>(), b_at = kABytes + columns_at<BW>();
+    const uint32_t a_at = ColumnsFragment<AW>::at(), b_at = kABytes + ColumnsFragment<BW>::at();
 
     if (steps > 0) load(0, 0);
     for (int step = 0; step < steps; ++step) {
-        wait_and_meet<0>();
+        loads_done<0>();
+        reads_done();
+        meet();
         if (step + 1 < steps) load(step + 1, (step + 1) % 2);
         const uint8_t* p = lds + step % 2 * kStage;
+        ColumnsFragment<AW> av[MT];
+        ColumnsFragment<BW> bv[NT];
 #pragma unroll
-        for (int s = 0; s < 2; ++s) {
-            bf16x8 av[MT], bv[NT];
+        for (int j = 0; j < NT; ++j) bv[j].read(p, b_at ^ (wn * NT + j) * 32);
 #pragma unroll
-            for (int j = 0; j < NT; ++j) bv[j] = columns_fragment<BW>(p, (b_at + s * 32 * BW) ^ (wn * NT + j) * 32);
-#pragma unroll
-            for (int i = 0; i < MT; ++i) av[i] = columns_fragment<AW>(p, (a_at + s * 32 * AW) ^ (wm * MT + i) * 32);
+        for (int i = 0; i < MT; ++i) av[i].read(p, a_at ^ (wm * MT + i) * 32);
+        const auto half = [&](auto h) {
+            constexpr int H = decltype(h)::value;
 #pragma unroll
             for (int i = 0; i < MT; ++i)
 #pragma unroll
                 for (int j = 0; j < NT; ++j)
-                    acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(bv[j], av[i], acc[i][j], 0, 0, 0);
+                    acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(bv[j].template half<H>(),
+                                                                        av[i].template half<H>(), acc[i][j], 0, 0, 0);
             if (sum_here) {
-                typedef uint32_t u32x4_ __attribute__((ext_vector_type(4)));
-                const bf16x8 ones = __builtin_bit_cast(bf16x8, u32x4_{0x3F803F80u, 0x3F803F80u, 0x3F803F80u,
-                                                                      0x3F803F80u});
+                const s16x8 ones = {0x3F80, 0x3F80, 0x3F80, 0x3F80, 0x3F80, 0x3F80, 0x3F80, 0x3F80};
 #pragma unroll
                 for (int i = 0; i < MT; ++i)
-                    sums[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(ones, av[i], sums[i], 0, 0, 0);
+                    sums[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, ones),
+                                                                      av[i].template half<H>(), sums[i], 0, 0, 0);
             }
-        }
+        };
+        half(std::integral_constant<int, 0>{});
+        half(std::integral_constant<int, 1>{});
     }
 
     const int pc = pair_column();

@@ -6,21 +6,12 @@
 namespace moe {
 namespace {
 
-constexpr int NT = 4;               // 16-column tiles of a wave
-constexpr int kCols = 64 * NT;      // columns of a workgroup's tile
-constexpr int kScalePieces = 16;    // scale bytes of a row fetched at a time: 4 steps
+constexpr int kCols = 256;       // columns of a workgroup's tile
+constexpr int kRows = 256;       // and up to so many rows
+constexpr int kScalePiece = 16;  // MXFP8 scale bytes of a row that pass through LDS at a time:
+constexpr int kScaleSteps = 4;   // those of so many steps
 
-template <int MT, bool BT, bool MX>
-struct Shape {
-    static constexpr int AJ = (MT + 1) / 2;
-    static constexpr int A_BYTES = AJ * 64 * kStepBytes;
-    static constexpr int STAGE = A_BYTES + kCols * kStepBytes;
-    static constexpr int SCALES = MX ? 2 * (AJ * 64 + kCols) * kScalePieces : 0;
-    static constexpr int FIT = (kLdsBytes - SCALES) / STAGE;
-    static constexpr int STAGES = FIT > 4 ? 4 : FIT;
-    static constexpr int LOADS = AJ + NT;  // of a wave, per stage
-    static_assert(STAGES >= 2, "a stage in flight beside the one multiplied");
-};
+constexpr int kBBytes = kCols * kStepBytes;
 
 // silu(g) u in fp32, as moe_swiglu has it.
 __device__ __forceinline__ float silu_mul(float g, float u) {
@@ -37,231 +28,278 @@ __device__ __forceinline__ void add8(float (&v)[8], const u32x4& b) {
 }
 __device__ __forceinline__ void store8(uint16_t* p, const float (&v)[8]) { *reinterpret_cast<u32x4*>(p) = pack8(v); }
 
-// 16 scale bytes from byte `at` of a row of n on; bytes past the row are 0.
-__device__ __forceinline__ u32x4 load_scale_piece(const uint8_t* row, int at, int n) {
-    u32x4 v = {0, 0, 0, 0};
-    if (at + kScalePieces <= n) {
-        __builtin_memcpy(&v, row + at, kScalePieces);
-    } else {
-#pragma unroll
-        for (int i = 0; i < kScalePieces; ++i)
-            if (at + i < n) v[i / 4] |= (uint32_t)row[at + i] << (i % 4 * 8);
+// A piece of the scale bytes of 16 LDS rows into LDS, a dword a lane: lane l has
+// bytes 4 (l % 4) .. + 3 of the row of scales that starts at byte `row` of buf.
+__device__ __forceinline__ void load_scale_piece(__amdgpu_buffer_rsrc_t buf, uint32_t row, int piece, uint32_t ld,
+                                                 bool dwords, uint8_t* lds) {
+    const uint32_t lane = threadIdx.x % kWave;
+    const uint32_t k = (uint32_t)piece * kScalePiece + lane % 4 * 4;
+    if (dwords) {
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(buf, (MOE_LDS void*)lds, 4, (int)(k < ld ? row + k : kPastEnd), 0, 0, 0);
+        return;
     }
-    return v;
+    uint32_t v = 0;
+#pragma unroll
+    for (uint32_t i = 0; i < 4; ++i) {
+        const uint32_t b = __builtin_amdgcn_raw_buffer_load_b8(buf, (int)(k + i < ld ? row + k + i : kPastEnd), 0, 0);
+        v |= (b & 0xFFu) << (i * 8);
+    }
+    *reinterpret_cast<uint32_t*>(lds + lane * 4) = v;
 }
 
-template <int MT, bool BT, bool MX, bool SWIGLU>
+template <int MH, bool BT, bool MX, bool SWIGLU>
 __device__ __forceinline__ void product(const GroupedArgs& g, const Tile& t, uint8_t* lds) {
-    using S = Shape<MT, BT, MX>;
+    constexpr int EL = MX ? 1 : 2;
+    constexpr int A_BYTES = MH * 64 * kStepBytes;
+    constexpr int B_AT = 2 * A_BYTES, SCALES_AT = B_AT + 2 * kBBytes;
+    constexpr int SCALE_BUF = (MH * 64 + kCols) * kScalePiece;
+    static_assert(SCALES_AT + (MX ? 2 * SCALE_BUF : 0) <= kLdsBytes, "two buffers of everything");
     const int lane = (int)(threadIdx.x % kWave), wave = (int)uniform(threadIdx.x / kWave);
     const int wm = wave / 4, wn = wave % 4;
-    constexpr int EL = MX ? 1 : 2;
     const int out_cols = SWIGLU ? g.N / 2 : g.N;
     const int col0 = t.col * (SWIGLU ? kCols / 2 : kCols);  // of the output
-    const uint32_t lda = (uint32_t)g.K * EL;
-    const int steps = (int)((lda + kStepBytes - 1) / kStepBytes);
+    const uint32_t ld = (uint32_t)g.K * EL;
+    const int steps = (int)((ld + kStepBytes - 1) / kStepBytes);
 
-    RowsOperand<S::AJ> a;
-    a.set(static_cast<const uint8_t*>(g.x) + (int64_t)t.first * lda, (int64_t)t.rows * lda, lda, wave * 8, 64);
-    RowsOperand<BT ? 1 : NT> br;
-    ColumnsOperand<BT ? NT : 1> bc;
-    const uint8_t* w = static_cast<const uint8_t*>(g.w) + (int64_t)t.e * g.N * g.K * EL;
+    // The tile's columns are in halves of 128, those of the rows of w from w_row[h] on:
+    // with SwiGLU the gates and the ups of the same 128.  A wave has 32 of either.
+    const int w_left = out_cols - col0;
+    const int64_t w_row = (int64_t)t.e * g.N + col0;
+    const int64_t w_row1 = w_row + (SWIGLU ? out_cols : 128);
+    const int w_left1 = SWIGLU ? w_left : max(w_left - 128, 0);
+    const uint8_t* w = static_cast<const uint8_t*>(g.w);
+
+    RowsOperand<MH> a;
+    a.set(ld);
+    const __amdgpu_buffer_rsrc_t a_buf =
+        grouped_buffer(static_cast<const uint8_t*>(g.x) + (int64_t)t.first * ld, (int64_t)t.rows * ld);
+    RowsOperand<2> br;
+    ColumnsOperand<4> bc;
+    __amdgpu_buffer_rsrc_t b_buf[2];
     if constexpr (BT) {  // w [K, N], the sum over its rows
-        bc.set(w + (int64_t)col0 * EL, (int64_t)g.K * g.N * EL - (int64_t)col0 * EL, (uint32_t)g.N * EL);
-    } else if constexpr (SWIGLU) {
-        // LDS rows 64 j + 0..31 are gate rows, 64 j + 32..63 the up rows of the same columns
-        const int64_t row = (int64_t)(wave / 4) * out_cols + col0;
-        br.set(w + row * lda, (int64_t)(out_cols - col0) * lda, lda, wave % 4 * 8, 32);
+        bc.set(w + ((int64_t)t.e * g.K * g.N + col0) * 2, ((int64_t)g.K * g.N - col0) * 2, (uint32_t)g.N * 2);
     } else {
-        br.set(w + (int64_t)col0 * lda, (int64_t)(g.N - col0) * lda, lda, wave * 8, 64);
+        br.set(ld);
+        b_buf[0] = grouped_buffer(w + w_row * ld, (int64_t)w_left * ld);
+        b_buf[1] = grouped_buffer(w + w_row1 * ld, (int64_t)w_left1 * ld);
     }
 
-    // MXFP8: thread i fetches the scales of LDS row i (of x, then of w), four
-    // steps at a time, one such piece ahead
-    const int scale_row = (int)threadIdx.x;
-    const bool has_scales = MX && scale_row < S::AJ * 64 + kCols;
-    const uint8_t* scale_base = nullptr;
-    u32x4 scale_next = {0, 0, 0, 0};
-    const int scale_n = g.K / 32;
-    if constexpr (MX) {
-        if (scale_row < S::AJ * 64) {
-            scale_base = g.xs + (int64_t)(t.first + min(scale_row, t.rows - 1)) * scale_n;
-        } else {
-            const int r = scale_row - S::AJ * 64;
-            const int row = SWIGLU ? min(col0 + r / 64 * 32 + r % 32, out_cols - 1) + (r % 64 / 32) * out_cols
-                                   : min(col0 + r, g.N - 1);
-            scale_base = g.ws + ((int64_t)t.e * g.N + (has_scales ? row : 0)) * scale_n;
+    // MXFP8 scales of the steps from `step` on: 16 LDS rows a load
+    const auto load_scales = [&](int step) {
+        const int piece = step / kScaleSteps;
+        const uint32_t n = (uint32_t)g.K / 32;
+        uint8_t* p = lds + SCALES_AT + piece % 2 * SCALE_BUF;
+        const __amdgpu_buffer_rsrc_t ab = grouped_buffer(g.xs + (int64_t)t.first * n, (int64_t)t.rows * n);
+#pragma unroll
+        for (int j = 0; j < (MH + 1) / 2; ++j) {
+            const int block = j * 8 + wave;
+            if (MH % 2 == 0 || block < 4 * MH)
+                load_scale_piece(ab, (uint32_t)(block * 16 + lane / 4) * n, piece, n, g.scale_dwords, p + block * 256);
         }
-        if (has_scales) scale_next = load_scale_piece(scale_base, 0, scale_n);
-    }
-    uint8_t* const lds_scales = lds + S::STAGES * S::STAGE;
-    constexpr int SCALE_BUF = (S::AJ * 64 + kCols) * kScalePieces;
-
-    const auto load = [&](int step, int buf) {
-        uint8_t* p = lds + buf * S::STAGE;
-        a.load(step, p);
-        if constexpr (BT)
-            bc.load(step, p + S::A_BYTES);
-        else
-            br.load(step, p + S::A_BYTES);
+        p += MH * 64 * kScalePiece;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const __amdgpu_buffer_rsrc_t wb =
+                grouped_buffer(g.ws + (h == 0 ? w_row : w_row1) * n, (int64_t)(h == 0 ? w_left : w_left1) * n);
+            load_scale_piece(wb, (uint32_t)(wave * 16 + lane / 4) * n, piece, n, g.scale_dwords,
+                             p + (h * 8 + wave) * 256);
+        }
     };
 
-    f32x4 acc[MT][NT];
+    f32x4 acc[2][MH][4];
 #pragma unroll
-    for (int i = 0; i < MT; ++i)
+    for (int h = 0; h < 2; ++h)
 #pragma unroll
-        for (int j = 0; j < NT; ++j) acc[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+        for (int i = 0; i < MH; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) acc[h][i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 
-    const uint32_t a_at = (uint32_t)(wm * MT * 16) * kStepBytes + rows_at(lane % 16, lane / 16);
-    const uint32_t b_at = S::A_BYTES + (BT ? columns_at<kCols * 2>()
-                                           : (uint32_t)(wn * NT * 16) * kStepBytes + rows_at(lane % 16, lane / 16));
+    using BFragment = std::conditional_t<BT, ColumnsFragment<kCols * 2>, RowsFragment>;
+    const uint32_t a_at = (uint32_t)(wm * MH * 16) * kStepBytes + RowsFragment::at();
+    const uint32_t b_at = B_AT + BFragment::at() + (BT ? 0u : (uint32_t)(wn * 32) * kStepBytes);
+    const uint32_t a_scale_at = SCALES_AT + (uint32_t)(wm * MH * 16 + lane % 16) * kScalePiece + lane / 16;
+    const uint32_t b_scale_at = SCALES_AT + (uint32_t)(MH * 64 + wn * 32 + lane % 16) * kScalePiece + lane / 16;
+    RowsFragment av[MH];
+    BFragment bv[2][2];
+    int a_scale[MH], b_scale[2][2];
+    int read_step = 0;
 
+    // Rows 0 of A are its first 32 MH: whole loads if MH is even; else the load that
+    // has both kinds of rows is quarter 3's, as rows 1 are.
+    constexpr int A1 = MH / 2, A3 = MH - A1;
+    constexpr int B1 = BT ? 0 : 2, B2 = BT ? 4 : 2;
+    // What quarter 0 does not need of a step: columns 1 and rows 1, or rows 1 alone, or
+    // rows 1 but for their first load.
+    constexpr int LEFT0 = MH % 2 == 1 ? A3 - 1 : BT ? A3 : B2 + A3;
+    run_steps<A1 + B1, B2, A3, LEFT0, A3>(
+        steps,
+        [&](auto half, int buf) {
+            constexpr int h = decltype(half)::value;
+            const uint8_t* p = lds + buf * A_BYTES;
 #pragma unroll
-    for (int s = 0; s < S::STAGES - 1; ++s)
-        if (s < steps) load(s, s);
-    int buf = 0;
-    for (int step = 0; step < steps; ++step) {
-        if constexpr (MX) {
-            if (step % 4 == 0 && has_scales)
-                *reinterpret_cast<u32x4*>(lds_scales + step / 4 % 2 * SCALE_BUF + scale_row * kScalePieces) = scale_next;
-        }
-        if (step + S::STAGES - 1 <= steps)
-            wait_and_meet<(S::STAGES - 2) * S::LOADS>();
-        else
-            wait_and_meet<0>();
-        if constexpr (MX) {
-            if (step % 4 == 0 && has_scales && step + 4 < steps)
-                scale_next = load_scale_piece(scale_base, (step / 4 + 1) * kScalePieces, scale_n);
-        }
-        const int ahead = buf == 0 ? S::STAGES - 1 : buf - 1;
-        if (step + S::STAGES - 1 < steps) load(step + S::STAGES - 1, ahead);
-        const uint8_t* p = lds + buf * S::STAGE;
-        if constexpr (MX) {
-            const uint8_t* sp = lds_scales + step / 4 % 2 * SCALE_BUF + step % 4 * 4 + lane / 16;
-            i32x8 bv[NT];
-            int bs[NT];
+            for (int i = 0; i < MH; ++i) av[i].read(p, a_at + (h * 2 * MH + i) * 2048);
+            if constexpr (MX) {
+                const uint8_t* sp = lds + read_step / kScaleSteps % 2 * SCALE_BUF + read_step % kScaleSteps * 4;
 #pragma unroll
-            for (int j = 0; j < NT; ++j) {
-                const i32x4 lo = *reinterpret_cast<const i32x4*>(p + b_at + j * 2048);
-                const i32x4 hi = *reinterpret_cast<const i32x4*>(p + ((b_at + j * 2048) ^ 64));
-                bv[j] = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
-                bs[j] = sp[(S::AJ * 64 + wn * NT * 16 + j * 16 + lane % 16) * kScalePieces];
+                for (int i = 0; i < MH; ++i) a_scale[i] = sp[a_scale_at + (h * 2 * MH + i) * 16 * kScalePiece];
+                read_step += h;
             }
+        },
+        [&](auto half, int buf) {
+            constexpr int h = decltype(half)::value;
+            const uint8_t* p = lds + buf * kBBytes;
 #pragma unroll
-            for (int i = 0; i < MT; ++i) {
-                const i32x4 lo = *reinterpret_cast<const i32x4*>(p + a_at + i * 2048);
-                const i32x4 hi = *reinterpret_cast<const i32x4*>(p + ((a_at + i * 2048) ^ 64));
-                const i32x8 av = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
-                const int as = sp[(wm * MT * 16 + i * 16 + lane % 16) * kScalePieces];
-#pragma unroll
-                for (int j = 0; j < NT; ++j)
-                    acc[i][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(bv[j], av, acc[i][j], 0, 0, 0, bs[j],
-                                                                                0, as);
+            for (int j = 0; j < 2; ++j) {
+                if constexpr (BT)
+                    bv[h][j].read(p, b_at ^ (h * 8 + wn * 2 + j) * 32);
+                else
+                    bv[h][j].read(p, b_at + (h * 8 + j) * 2048);
             }
-        } else {
+            if constexpr (MX) {
+                const uint8_t* sp = lds + read_step / kScaleSteps % 2 * SCALE_BUF + read_step % kScaleSteps * 4;
 #pragma unroll
-            for (int s = 0; s < 2; ++s) {
-                bf16x8 av[MT], bv[NT];
+                for (int j = 0; j < 2; ++j) b_scale[h][j] = sp[b_scale_at + (h * 8 + j) * 16 * kScalePiece];
+            }
+        },
+        [&](auto half_a, auto half_b) {
+            constexpr int ha = decltype(half_a)::value, hb = decltype(half_b)::value;
+            if constexpr (MX) {
 #pragma unroll
-                for (int j = 0; j < NT; ++j) {
-                    if constexpr (BT)
-                        bv[j] = columns_fragment<kCols * 2>(p, (b_at + s * 32 * kCols * 2) ^ (wn * NT + j) * 32);
-                    else
-                        bv[j] = *reinterpret_cast<const bf16x8*>(p + ((b_at + j * 2048) ^ s * 64));
+                for (int i = 0; i < MH; ++i)
+#pragma unroll
+                    for (int j = 0; j < 2; ++j)
+                        acc[ha][i][hb * 2 + j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
+                            bv[hb][j].whole(), av[i].whole(), acc[ha][i][hb * 2 + j], 0, 0, 0, b_scale[hb][j], 0,
+                            a_scale[i]);
+            } else {
+#pragma unroll
+                for (int i = 0; i < MH; ++i)
+#pragma unroll
+                    for (int j = 0; j < 2; ++j)
+                        acc[ha][i][hb * 2 + j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+                            bv[hb][j].template half<0>(), av[i].template half<0>(), acc[ha][i][hb * 2 + j], 0, 0, 0);
+#pragma unroll
+                for (int i = 0; i < MH; ++i)
+#pragma unroll
+                    for (int j = 0; j < 2; ++j)
+                        acc[ha][i][hb * 2 + j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+                            bv[hb][j].template half<1>(), av[i].template half<1>(), acc[ha][i][hb * 2 + j], 0, 0, 0);
+            }
+        },
+        [&](auto quarter, int step, int buf) {
+            constexpr int q = decltype(quarter)::value;
+            uint8_t* pa = lds + buf * A_BYTES;
+            uint8_t* pb = lds + B_AT + buf * kBBytes;
+            if constexpr (q == 1) {
+                if constexpr (MX) {
+                    if (step % kScaleSteps == 0) load_scales(step);
                 }
-#pragma unroll
-                for (int i = 0; i < MT; ++i)
-                    av[i] = *reinterpret_cast<const bf16x8*>(p + ((a_at + i * 2048) ^ s * 64));
-#pragma unroll
-                for (int i = 0; i < MT; ++i)
-#pragma unroll
-                    for (int j = 0; j < NT; ++j)
-                        acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(bv[j], av[i], acc[i][j], 0, 0, 0);
+                a.template load<0, A1>(a_buf, step, pa);
+                if constexpr (!BT) br.template load<0, 2>(b_buf[0], step, pb);
+            } else if constexpr (q == 2) {
+                if constexpr (BT)
+                    bc.load(step, pb);
+                else
+                    br.template load<0, 2>(b_buf[1], step, pb + kBBytes / 2);
+            } else {
+                a.template load<A1, MH>(a_buf, step, pa + A1 * 64 * kStepBytes);
             }
-        }
-        buf = buf + 1 == S::STAGES ? 0 : buf + 1;
-    }
+        });
 
-    // epilogue: 8 columns of one row a lane and tile pair
-    const int pc = pair_column();
-    u32x4 bias[NT / 2];  // of the pairs' columns; behind SwiGLU of gate and up
+    // epilogue: eight columns of one row a lane, of two tiles of 16, once behind SwiGLU
+    // and twice without.  Bias and residual are all asked for before the first use: one
+    // after the other, behind the stores, they took a third of the time (8192 x 7168 x
+    // 2048 with a residual: 276 us, now 261).
+    constexpr int OUT = SWIGLU ? 1 : 2;
+    const int col = col0 + wn * 32 + pair_column();
+    u32x4 bias[2], residual[2][MH][OUT];  // bias behind SwiGLU: of gate and up
     if (g.bias != nullptr) {
 #pragma unroll
-        for (int j = 0; j < NT / 2; ++j) {
-            const int c = col0 + (SWIGLU ? wn * 32 : wn * NT * 16 + j * 32) + pc;
+        for (int j = 0; j < 2; ++j) {
+            const int c = SWIGLU ? col : col + j * 128;
             if (c < out_cols) bias[j] = load8(g.bias + (int64_t)t.e * g.N + c + (SWIGLU ? j * out_cols : 0));
         }
     }
+    const auto row_of = [&](int h, int i) { return ((h * 2 + wm) * MH + i) * 16 + lane % 16; };
+    if (g.residual != nullptr) {
 #pragma unroll
-    for (int i = 0; i < MT; ++i) {
-        const int m = wm * MT * 16 + i * 16 + lane % 16;
-        const int64_t row = t.first + m;
-        if constexpr (SWIGLU) {
-            float gate[8], up[8];
-            pair_values(acc[i][0], acc[i][1], gate);
-            pair_values(acc[i][2], acc[i][3], up);
-            const int c = col0 + wn * 32 + pc;
-            if (m < t.rows && c < out_cols) {
-                if (g.bias != nullptr) {
-                    add8(gate, bias[0]);
-                    add8(up, bias[1]);
-                }
-                if (g.pre != nullptr) {
-                    store8(g.pre + row * g.N + c, gate);
-                    store8(g.pre + row * g.N + out_cols + c, up);
-                }
+        for (int h = 0; h < 2; ++h)
 #pragma unroll
-                for (int q = 0; q < 8; ++q) gate[q] = silu_mul(gate[q], up[q]);
-                if (g.residual != nullptr) add8(gate, load8(g.residual + row * out_cols + c));
-                store8(g.out + row * out_cols + c, gate);
+            for (int i = 0; i < MH; ++i)
+#pragma unroll
+                for (int j = 0; j < OUT; ++j) {
+                    const int m = row_of(h, i), c = col + j * 128;
+                    if (m < t.rows && c < out_cols)
+                        residual[h][i][j] = load8(g.residual + (int64_t)(t.first + m) * out_cols + c);
+                }
+    }
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int i = 0; i < MH; ++i) {
+            const int m = row_of(h, i);
+            const int64_t row = t.first + m;
+            float v[2][8];
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                pair_values(acc[h][i][2 * j], acc[h][i][2 * j + 1], v[j]);
+                if (g.bias != nullptr) add8(v[j], bias[j]);
             }
-        } else {
+            if constexpr (SWIGLU) {
+                if (g.pre != nullptr && m < t.rows && col < out_cols) {
+                    store8(g.pre + row * g.N + col, v[0]);
+                    store8(g.pre + row * g.N + out_cols + col, v[1]);
+                }
 #pragma unroll
-            for (int j = 0; j < NT; j += 2) {
-                float v[8];
-                pair_values(acc[i][j], acc[i][j + 1], v);
-                const int c = col0 + (wn * NT + j) * 16 + pc;
+                for (int q = 0; q < 8; ++q) v[0][q] = silu_mul(v[0][q], v[1][q]);
+            }
+#pragma unroll
+            for (int j = 0; j < OUT; ++j) {
+                const int c = col + j * 128;
                 if (m < t.rows && c < out_cols) {
-                    if (g.bias != nullptr) add8(v, bias[j / 2]);
-                    if (g.residual != nullptr) add8(v, load8(g.residual + row * out_cols + c));
-                    store8(g.out + row * out_cols + c, v);
+                    if (g.residual != nullptr) add8(v[j], residual[h][i][j]);
+                    store8(g.out + row * out_cols + c, v[j]);
                 }
             }
         }
-    }
 }
 
 template <bool BT, bool MX, bool SWIGLU>
-__global__ __launch_bounds__(kGroupedThreads) void grouped_kernel(GroupedArgs g, int col_tiles) {
+__global__ __launch_bounds__(kGroupedThreads, 2) void grouped_kernel(GroupedArgs g, int col_tiles, int whole) {
     __shared__ __align__(16) uint8_t lds[kLdsBytes];
-    const Tile t = find_tile(g.rows, col_tiles);
-    if (t.e < 0) return;
-    if (t.last_rows > 192)
-        product<8, BT, MX, SWIGLU>(g, t, lds);
-    else if (t.last_rows > 128)
-        product<6, BT, MX, SWIGLU>(g, t, lds);
-    else if (t.last_rows > 64)
+    const Tile t = find_tile(g.rows, col_tiles, whole);
+    if (t.rows == 0) return;
+    if (t.rows > 192)
         product<4, BT, MX, SWIGLU>(g, t, lds);
-    else if (t.last_rows > 32)
+    else if (t.rows > 128)
+        product<3, BT, MX, SWIGLU>(g, t, lds);
+    else if (t.rows > 64)
         product<2, BT, MX, SWIGLU>(g, t, lds);
     else
         product<1, BT, MX, SWIGLU>(g, t, lds);
 }
 
+constexpr int kCus = 256;
+
 template <bool BT, bool MX, bool SWIGLU>
 hipError_t launch(const GroupedArgs& g, hipStream_t stream) {
     const int cols = SWIGLU ? kCols / 2 : kCols, out_cols = SWIGLU ? g.N / 2 : g.N;
     const int col_tiles = (out_cols + cols - 1) / cols;
-    const int64_t tiles = grouped_tiles(g.rows, col_tiles);
+    // Fewer rows a tile where whole ones would leave CUs without work; rows spread
+    // evenly over the experts, as far as the host can know.
+    const int experts = g.rows.E < g.rows.R ? g.rows.E : g.rows.R;
+    int whole = kRows;
+    while (whole > 64 && (int64_t)experts * ((g.rows.R / experts + whole - 1) / whole) * col_tiles < kCus) whole /= 2;
+    const int64_t tiles = grouped_tiles(g.rows, whole, col_tiles);
     const uint32_t grid = (uint32_t)((tiles + 7) / 8 * 8);
-    grouped_kernel<BT, MX, SWIGLU><<<grid, kGroupedThreads, 0, stream>>>(g, col_tiles);
+    grouped_kernel<BT, MX, SWIGLU><<<grid, kGroupedThreads, 0, stream>>>(g, col_tiles, whole);
     return hipGetLastError();
 }
 
 }  // namespace
 
-int64_t grouped_linear_tiles(const GroupedRows& rows, int cols, bool swiglu) {
-    return grouped_tiles(rows, swiglu ? (cols / 2 + kCols / 2 - 1) / (kCols / 2) : (cols + kCols - 1) / kCols);
+int64_t grouped_linear_tiles(const GroupedRows& rows, int cols) {
+    return grouped_tiles(rows, 64, (cols + kCols - 1) / kCols);
 }
 
 hipError_t launch_grouped_linear(const GroupedArgs& g, bool swiglu, hipStream_t stream) {

@@ -261,17 +261,16 @@ hipError_t launch_linear_mxfp4(const void* x, int T, int K, const uint8_t* w, co
                                hipStream_t stream);
 
 // -------------------------------------------- experts' products and gradients
-constexpr int kGroupedRows = 256;  // rows of a whole tile
 struct GroupedRows {
     const int32_t* offsets;  // [E+1] on the device, or null: one expert has all R rows
     const int32_t* counts;   // [E], or null: a segment ends where the next begins
     int E, R;
 };
-// Workgroups that any E segments of R rows take: one per row tile and column tile.
-inline int64_t grouped_tiles(const GroupedRows& g, int col_tiles) {
+// Workgroups that any E segments of R rows take at most: one per row tile of up to
+// `whole` rows and column tile.
+inline int64_t grouped_tiles(const GroupedRows& g, int whole, int col_tiles) {
     const int64_t partial = g.E < g.R ? g.E : g.R;
-    return (g.offsets == nullptr ? (g.R + kGroupedRows - 1) / kGroupedRows : g.R / kGroupedRows + partial) *
-           (int64_t)col_tiles;
+    return (g.offsets == nullptr ? ((int64_t)g.R + whole - 1) / whole : g.R / whole + partial) * (int64_t)col_tiles;
 }
 // out = act(x w_e^T + bias_e) + residual; as grad_x: out = x w_e, x being dy and w [K, N].
 struct GroupedArgs {
@@ -285,8 +284,10 @@ struct GroupedArgs {
     int N, K;
     uint16_t* out;            // bf16 [R, N], or [R, N/2] behind SwiGLU
     uint16_t* pre;            // bf16 [R, N] or null: the rows before SwiGLU
+    bool scale_dwords;        // rows of xs and ws are whole aligned dwords
 };
-int64_t grouped_linear_tiles(const GroupedRows& rows, int cols, bool swiglu);
+// Workgroups of the smallest tiles, for rows of `cols` columns (N, before SwiGLU).
+int64_t grouped_linear_tiles(const GroupedRows& rows, int cols);
 hipError_t launch_grouped_linear(const GroupedArgs& g, bool swiglu, hipStream_t stream);
 hipError_t launch_grouped_grad_x(const GroupedArgs& g, hipStream_t stream);
 struct GroupedGradArgs {
