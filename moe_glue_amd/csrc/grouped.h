@@ -307,6 +307,14 @@ __device__ __forceinline__ void run_steps(int steps, const ReadA& read_a, const 
     loads_done<0>();  // none may land in the next workgroup's LDS
 }
 
+// The sum of a value over the four 16-lane rows, in every lane.
+__device__ __forceinline__ uint32_t across_rows(uint32_t v) {
+    const auto p = __builtin_amdgcn_permlane16_swap(v, v, false, false);
+    v = apply<Op::FAdd>(p[0], p[1]);
+    const auto q = __builtin_amdgcn_permlane32_swap(v, v, false, false);
+    return apply<Op::FAdd>(q[0], q[1]);
+}
+
 // Eight neighbouring columns of one row of D, of the tile pair (a, b): see
 // pair_column() for which.  Quarter q of a row of 16 lanes holds columns 4 q .. of
 // both tiles; the swap of odd rows of a with even rows of b gives lanes of even
