@@ -108,13 +108,44 @@ __device__ __forceinline__ Tile find_tile(const GroupedRows& g, int col_tiles, i
             min((each + (m < more ? 1 : 0)) * 64, n - first), at / in_group};
 }
 
-// ------------------------------------------------------------------- loads
-__device__ __forceinline__ __amdgpu_buffer_rsrc_t grouped_buffer(const void* p, int64_t bytes) {
-    const int64_t n = bytes < 0 ? 0 : bytes > (int64_t)kPastEnd ? (int64_t)kPastEnd : bytes;
-    return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), 0, (int)(uint32_t)n, kRawBufferWord3);
+template <int N, class F>
+__device__ __forceinline__ void unrolled(F&& f) {
+    if constexpr (N > 0) {
+        unrolled<N - 1>(f);
+        f(std::integral_constant<int, N - 1>{});
+    }
 }
-__device__ __forceinline__ void load_to_lds(__amdgpu_buffer_rsrc_t r, uint32_t lane, uint32_t scalar, uint8_t* lds) {
-    __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (MOE_LDS void*)lds, 16, (int)lane, (int)scalar, 0, 0);
+
+// ------------------------------------------------------------------- loads
+__device__ __forceinline__ int grouped_bytes(int64_t bytes) {
+    return (int)(uint32_t)(bytes < 0 ? 0 : bytes > (int64_t)kPastEnd ? (int64_t)kPastEnd : bytes);
+}
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t grouped_buffer(const void* p, int64_t bytes) {
+    return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), 0, grouped_bytes(bytes), kRawBufferWord3);
+}
+typedef __attribute__((ext_vector_type(4))) int BufferWords;
+__device__ __forceinline__ BufferWords buffer_words(const void* p, int64_t bytes) {
+    const uint64_t at = reinterpret_cast<uint64_t>(p);
+    return {(int)(uint32_t)at, (int)((uint32_t)(at >> 32) & 0xFFFFu), grouped_bytes(bytes), kRawBufferWord3};
+}
+// 16 bytes (or a dword) a lane from byte lane + scalar of a buffer to LDS, the wave's one
+// behind the other.  In assembly, for behind the builtin the compiler takes a transposing
+// LDS read for one of what is in flight, whatever buffer it goes to, and waits for all
+// loads before it (grad_w of 128 experts, 1536 x 2048: 423 us, GRAD_US without).  There is
+// no register to write; waiting is the caller's (loads_done).  M0 holds the LDS address,
+// and the wait state is the one it asks for before a load to LDS; nothing else in these
+// kernels uses M0.
+__device__ __forceinline__ void load_to_lds(const BufferWords& r, uint32_t lane, uint32_t scalar, uint8_t* lds) {
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds" ::"s"(
+                     (uint32_t)(uintptr_t)(MOE_LDS uint8_t*)lds),
+                 "v"(lane), "s"(r), "s"(scalar)
+                 : "memory");
+}
+__device__ __forceinline__ void load_dword_to_lds(const BufferWords& r, uint32_t lane, uint8_t* lds) {
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dword %1, %2, 0 offen lds" ::"s"(
+                     (uint32_t)(uintptr_t)(MOE_LDS uint8_t*)lds),
+                 "v"(lane), "s"(r)
+                 : "memory");
 }
 
 // An operand with the summed index along its rows, of `ld` bytes each; load j of a
@@ -135,7 +166,7 @@ struct RowsOperand {
     // Loads FROM .. TO - 1 of a step, the first of them to LDS row 0.  Steps in order:
     // from the one that holds a row's end on, lanes past it stay turned away.
     template <int FROM, int TO>
-    __device__ __forceinline__ void load(__amdgpu_buffer_rsrc_t buf, int step, uint8_t* lds) {
+    __device__ __forceinline__ void load(const BufferWords& buf, int step, uint8_t* lds) {
         const uint32_t wave = uniform(threadIdx.x / kWave);
         const uint32_t k = (uint32_t)step * kStepBytes;
         if (k + kStepBytes > ld) {
@@ -148,16 +179,16 @@ struct RowsOperand {
     }
 };
 
-// An operand with the summed index across its rows: rows [0, sum) of `ld` bytes
-// from base on (base: the first column of the tile), W bytes of each; J loads a
-// wave of 64 rows.
-template <int J>
+// An operand with the summed index across its rows, of `ld` bytes each, in `bytes`
+// bytes from base (the first column of the tile) on: K rows a step, W bytes of each,
+// by a workgroup of WAVES waves.  Rows past the end read zeros.
+template <int W, int K, int WAVES>
 struct ColumnsOperand {
-    static constexpr int W = J * 128;  // 64 rows * W = J * 8 KiB
-    static constexpr int LDS_BYTES = 64 * W;
+    static constexpr int LDS_BYTES = K * W;
+    static constexpr int LOADS = LDS_BYTES / (WAVES * 1024);  // of a wave, per step
     const uint8_t* base;
-    int64_t bytes;  // from base to the end of the last row
-    uint32_t at[J];
+    int64_t bytes;
+    uint32_t at[LOADS];
     uint32_t ld;
     __device__ __forceinline__ void set(const uint8_t* base_, int64_t bytes_, uint32_t ld_) {
         constexpr uint32_t ROWS = 1024 / W, PIECES = W / 16;
@@ -166,19 +197,24 @@ struct ColumnsOperand {
         bytes = bytes_;
         ld = ld_;
 #pragma unroll
-        for (int j = 0; j < J; ++j) {
-            const uint32_t row = (j * 8 + wave) * ROWS + lane / PIECES;
+        for (int j = 0; j < LOADS; ++j) {
+            const uint32_t row = (j * WAVES + wave) * ROWS + lane / PIECES;
             const uint32_t key = row % 4 + row / 8 % 2 * 4;
             const uint32_t piece = lane % PIECES;
             at[j] = row * ld + ((piece / 2 ^ key) * 2 + piece % 2) * 16;
         }
     }
-    __device__ __forceinline__ void load(int step, uint8_t* lds) {
-        const uint32_t wave = uniform(threadIdx.x / kWave);
-        const int64_t from = (int64_t)step * 64 * ld;
-        const __amdgpu_buffer_rsrc_t buf = grouped_buffer(base + from, bytes - from);
-#pragma unroll
-        for (int j = 0; j < J; ++j) load_to_lds(buf, at[j], 0, lds + (j * 8 + wave) * 1024);
+    __device__ __forceinline__ BufferWords buffer(int step) const {
+        const int64_t from = (int64_t)step * K * ld;
+        return buffer_words(base + from, bytes - from);
+    }
+    template <int J>  // load J of a step
+    __device__ __forceinline__ void load_one(const BufferWords& buf, uint8_t* lds) const {
+        load_to_lds(buf, at[J], 0, lds + (J * WAVES + uniform(threadIdx.x / kWave)) * 1024);
+    }
+    __device__ __forceinline__ void load(int step, uint8_t* lds) const {
+        const BufferWords buf = buffer(step);
+        unrolled<LOADS>([&](auto j) { load_one<decltype(j)::value>(buf, lds); });
     }
 };
 
@@ -201,9 +237,9 @@ struct RowsFragment {
     }
     __device__ __forceinline__ i32x8 whole() const { return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7); }
 };
-template <int W>  // bytes of an LDS row
+template <int W, int K>  // bytes of an LDS row, rows of a step: 32 or 64
 struct ColumnsFragment {
-    s16x4 v[4];
+    s16x4 v[K / 16];
     // The lane's place for unit 0: xor the unit's 32 bytes in.
     static __device__ __forceinline__ uint32_t at() {
         const uint32_t lane = threadIdx.x % kWave;
@@ -212,7 +248,7 @@ struct ColumnsFragment {
     }
     __device__ __forceinline__ void read(const uint8_t* p, uint32_t at) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i)  // k 0..3, 4..7 of the lane's eight, of either 32
+        for (int i = 0; i < K / 16; ++i)  // k 0..3, 4..7 of the lane's eight, of every 32
             v[i] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((MOE_LDS s16x4*)(p + at + (i / 2 * 32 + i % 2 * 4) * W));
     }
     template <int H>
@@ -220,14 +256,6 @@ struct ColumnsFragment {
         return __builtin_bit_cast(bf16x8, __builtin_shufflevector(v[2 * H], v[2 * H + 1], 0, 1, 2, 3, 4, 5, 6, 7));
     }
 };
-
-template <int N, class F>
-__device__ __forceinline__ void unrolled(F&& f) {
-    if constexpr (N > 0) {
-        unrolled<N - 1>(f);
-        f(std::integral_constant<int, N - 1>{});
-    }
-}
 
 // ------------------------------------------------------------------- steps
 __device__ __forceinline__ void meet() {

@@ -29,15 +29,16 @@ __device__ __forceinline__ void add8(float (&v)[8], const u32x4& b) {
 __device__ __forceinline__ void store8(uint16_t* p, const float (&v)[8]) { *reinterpret_cast<u32x4*>(p) = pack8(v); }
 
 // A piece of the scale bytes of 16 LDS rows into LDS, a dword a lane: lane l has
-// bytes 4 (l % 4) .. + 3 of the row of scales that starts at byte `row` of buf.
-__device__ __forceinline__ void load_scale_piece(__amdgpu_buffer_rsrc_t buf, uint32_t row, int piece, uint32_t ld,
+// bytes 4 (l % 4) .. + 3 of the row of scales that starts at byte `row` from base on.
+__device__ __forceinline__ void load_scale_piece(const uint8_t* base, int64_t bytes, uint32_t row, int piece, uint32_t ld,
                                                  bool dwords, uint8_t* lds) {
     const uint32_t lane = threadIdx.x % kWave;
     const uint32_t k = (uint32_t)piece * kScalePiece + lane % 4 * 4;
     if (dwords) {
-        __builtin_amdgcn_raw_ptr_buffer_load_lds(buf, (MOE_LDS void*)lds, 4, (int)(k < ld ? row + k : kPastEnd), 0, 0, 0);
+        load_dword_to_lds(buffer_words(base, bytes), k < ld ? row + k : kPastEnd, lds);
         return;
     }
+    const __amdgpu_buffer_rsrc_t buf = grouped_buffer(base, bytes);
     uint32_t v = 0;
 #pragma unroll
     for (uint32_t i = 0; i < 4; ++i) {
@@ -71,17 +72,17 @@ __device__ __forceinline__ void product(const GroupedArgs& g, const Tile& t, uin
 
     RowsOperand<MH> a;
     a.set(ld);
-    const __amdgpu_buffer_rsrc_t a_buf =
-        grouped_buffer(static_cast<const uint8_t*>(g.x) + (int64_t)t.first * ld, (int64_t)t.rows * ld);
+    const BufferWords a_buf =
+        buffer_words(static_cast<const uint8_t*>(g.x) + (int64_t)t.first * ld, (int64_t)t.rows * ld);
     RowsOperand<2> br;
-    ColumnsOperand<4> bc;
-    __amdgpu_buffer_rsrc_t b_buf[2];
+    ColumnsOperand<kCols * 2, 64, 8> bc;
+    BufferWords b_buf[2];
     if constexpr (BT) {  // w [K, N], the sum over its rows
         bc.set(w + ((int64_t)t.e * g.K * g.N + col0) * 2, ((int64_t)g.K * g.N - col0) * 2, (uint32_t)g.N * 2);
     } else {
         br.set(ld);
-        b_buf[0] = grouped_buffer(w + w_row * ld, (int64_t)w_left * ld);
-        b_buf[1] = grouped_buffer(w + w_row1 * ld, (int64_t)w_left1 * ld);
+        b_buf[0] = buffer_words(w + w_row * ld, (int64_t)w_left * ld);
+        b_buf[1] = buffer_words(w + w_row1 * ld, (int64_t)w_left1 * ld);
     }
 
     // MXFP8 scales of the steps from `step` on: 16 LDS rows a load
@@ -89,20 +90,18 @@ __device__ __forceinline__ void product(const GroupedArgs& g, const Tile& t, uin
         const int piece = step / kScaleSteps;
         const uint32_t n = (uint32_t)g.K / 32;
         uint8_t* p = lds + SCALES_AT + piece % 2 * SCALE_BUF;
-        const __amdgpu_buffer_rsrc_t ab = grouped_buffer(g.xs + (int64_t)t.first * n, (int64_t)t.rows * n);
 #pragma unroll
         for (int j = 0; j < (MH + 1) / 2; ++j) {
             const int block = j * 8 + wave;
             if (MH % 2 == 0 || block < 4 * MH)
-                load_scale_piece(ab, (uint32_t)(block * 16 + lane / 4) * n, piece, n, g.scale_dwords, p + block * 256);
+                load_scale_piece(g.xs + (int64_t)t.first * n, (int64_t)t.rows * n,
+                                 (uint32_t)(block * 16 + lane / 4) * n, piece, n, g.scale_dwords, p + block * 256);
         }
         p += MH * 64 * kScalePiece;
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-            const __amdgpu_buffer_rsrc_t wb =
-                grouped_buffer(g.ws + (h == 0 ? w_row : w_row1) * n, (int64_t)(h == 0 ? w_left : w_left1) * n);
-            load_scale_piece(wb, (uint32_t)(wave * 16 + lane / 4) * n, piece, n, g.scale_dwords,
-                             p + (h * 8 + wave) * 256);
+            load_scale_piece(g.ws + (h == 0 ? w_row : w_row1) * n, (int64_t)(h == 0 ? w_left : w_left1) * n,
+                             (uint32_t)(wave * 16 + lane / 4) * n, piece, n, g.scale_dwords, p + (h * 8 + wave) * 256);
         }
     };
 
@@ -114,7 +113,7 @@ __device__ __forceinline__ void product(const GroupedArgs& g, const Tile& t, uin
 #pragma unroll
             for (int j = 0; j < 4; ++j) acc[h][i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 
-    using BFragment = std::conditional_t<BT, ColumnsFragment<kCols * 2>, RowsFragment>;
+    using BFragment = std::conditional_t<BT, ColumnsFragment<kCols * 2, 64>, RowsFragment>;
     const uint32_t a_at = (uint32_t)(wm * MH * 16) * kStepBytes + RowsFragment::at();
     const uint32_t b_at = B_AT + BFragment::at() + (BT ? 0u : (uint32_t)(wn * 32) * kStepBytes);
     const uint32_t a_scale_at = SCALES_AT + (uint32_t)(wm * MH * 16 + lane % 16) * kScalePiece + lane / 16;
