@@ -71,12 +71,14 @@ struct Tile {
 };
 
 // The tile of this workgroup.  Tiles are numbered expert by expert; in an expert,
-// groups of kTogether row tiles by column tile by row tile.  Each XCD (workgroups
-// b with equal b % 8) takes one run of them, so that the weights that row tiles
-// share, and the rows that column tiles share, meet in its L2.  Every wave looks for
-// itself: a lane sums the tiles of up to 8 experts and the wave's prefix sums find the
-// lane that holds the tile; then its experts, one a lane, the same way.
-constexpr int kTogether = 8;
+// groups of kTogether row tiles by column tile by row tile.  The XCDs (workgroups b with
+// equal b % 8) take kRun tiles each by turns, so that
+// the weights that row tiles share, and the rows that column tiles share, meet in its
+// L2, and an expert with many rows is not one XCD's alone (64 experts under skewed
+// routing, MXFP8: 187 us with an eighth of all tiles at a stretch, 171 so).  Every wave
+// looks for itself: a lane sums the tiles of up to 8 experts and the wave's prefix sums
+// find the lane that holds the tile; then its experts, one a lane, the same way.
+constexpr int kTogether = 8, kRun = 8;
 __device__ __forceinline__ Tile find_tile(const GroupedRows& g, int col_tiles, int whole) {
     const int lane = (int)(threadIdx.x % kWave);
     const int per = (g.E + kWave - 1) / kWave;
@@ -87,9 +89,10 @@ __device__ __forceinline__ Tile find_tile(const GroupedRows& g, int col_tiles, i
     }
     const int upto = wave_inclusive_sum(mine);
     const int total = __builtin_amdgcn_readlane(upto, kWave - 1) * col_tiles;
-    const int run = (total + 7) / 8;
-    const int u = (int)(blockIdx.x % 8) * run + (int)(blockIdx.x / 8);
-    if ((int)(blockIdx.x / 8) >= run || u >= total) return {0, 0, 0, 0};
+    const uint32_t run = min((uint32_t)(total + 7) / 8, (uint32_t)kRun);
+    if (total == 0) return {0, 0, 0, 0};
+    const int u = (int)(blockIdx.x / 8 / run * (8 * run) + blockIdx.x % 8 * run + blockIdx.x / 8 % run);
+    if (u >= total) return {0, 0, 0, 0};
     const int owner = __builtin_ctzll(__ballot(upto * col_tiles > u));
     const int before = __builtin_amdgcn_readlane(upto - mine, owner);
     Segment s = {0, 0};

@@ -290,7 +290,7 @@ hipError_t launch(const GroupedArgs& g, hipStream_t stream) {
     int whole = kRows;
     while (whole > 64 && (int64_t)experts * ((g.rows.R / experts + whole - 1) / whole) * col_tiles < kCus) whole /= 2;
     const int64_t tiles = grouped_tiles(g.rows, whole, col_tiles);
-    const uint32_t grid = (uint32_t)((tiles + 7) / 8 * 8);
+    const uint32_t grid = (uint32_t)((tiles + 8 * kRun - 1) / (8 * kRun) * (8 * kRun));  // whole turns
     grouped_kernel<BT, MX, SWIGLU><<<grid, kGroupedThreads, 0, stream>>>(g, col_tiles, whole);
     return hipGetLastError();
 }
