@@ -338,6 +338,26 @@ __device__ __forceinline__ void run_steps(int steps, const ReadA& read_a, const 
     loads_done<0>();  // none may land in the next workgroup's LDS
 }
 
+// The steps of a tile of few rows, whose quarters would be a few instructions between
+// barriers: STAGES buffers by turns, one barrier a step, all waves abreast.  load(step,
+// buffer) issues the LOADS loads of a wave of a step, also behind the last (zeros then).
+template <int STAGES, int LOADS, class Compute, class Load>
+__device__ __forceinline__ void run_short_steps(int steps, const Compute& compute, const Load& load) {
+    if (steps == 0) return;
+#pragma unroll
+    for (int s = 0; s < STAGES - 1; ++s) load(s, s);
+    int buf = 0;
+    for (int step = 0; step < steps; ++step) {
+        loads_done<(STAGES - 2) * LOADS>();
+        reads_done();  // of the step before, whose buffer is the one that is loaded now
+        meet();
+        load(step + STAGES - 1, buf == 0 ? STAGES - 1 : buf - 1);
+        compute(buf);
+        buf = buf + 1 == STAGES ? 0 : buf + 1;
+    }
+    loads_done<0>();  // none may land in the next workgroup's LDS
+}
+
 // The sum of a value over the four 16-lane rows, in every lane.
 __device__ __forceinline__ uint32_t across_rows(uint32_t v) {
     const auto p = __builtin_amdgcn_permlane16_swap(v, v, false, false);

@@ -12,6 +12,7 @@ constexpr int kScalePiece = 16;  // MXFP8 scale bytes of a row that pass through
 constexpr int kScaleSteps = 4;   // those of so many steps
 
 constexpr int kBBytes = kCols * kStepBytes;
+constexpr int kShortMH = 1;      // tiles of up to 64 of these rows take the short steps
 
 // silu(g) u in fp32, as moe_swiglu has it.
 __device__ __forceinline__ float silu_mul(float g, float u) {
@@ -52,9 +53,11 @@ template <int MH, bool BT, bool MX, bool SWIGLU>
 __device__ __forceinline__ void product(const GroupedArgs& g, const Tile& t, uint8_t* lds) {
     constexpr int EL = MX ? 1 : 2;
     constexpr int A_BYTES = MH * 64 * kStepBytes;
-    constexpr int B_AT = 2 * A_BYTES, SCALES_AT = B_AT + 2 * kBBytes;
     constexpr int SCALE_BUF = (MH * 64 + kCols) * kScalePiece;
-    static_assert(SCALES_AT + (MX ? 2 * SCALE_BUF : 0) <= kLdsBytes, "two buffers of everything");
+    constexpr bool SHORT = MH <= kShortMH;
+    constexpr int STAGES = SHORT ? (kLdsBytes - (MX ? 2 * SCALE_BUF : 0)) / (A_BYTES + kBBytes) : 2;
+    constexpr int B_AT = STAGES * A_BYTES, SCALES_AT = B_AT + STAGES * kBBytes;
+    static_assert(STAGES >= (SHORT ? 3 : 2) && SCALES_AT + (MX ? 2 * SCALE_BUF : 0) <= kLdsBytes, "the steps in LDS");
     const int lane = (int)(threadIdx.x % kWave), wave = (int)uniform(threadIdx.x / kWave);
     const int wm = wave / 4, wn = wave % 4;
     const int out_cols = SWIGLU ? g.N / 2 : g.N;
@@ -130,80 +133,101 @@ __device__ __forceinline__ void product(const GroupedArgs& g, const Tile& t, uin
     // What quarter 0 does not need of a step: columns 1 and rows 1, or rows 1 alone, or
     // rows 1 but for their first load.
     constexpr int LEFT0 = MH % 2 == 1 ? A3 - 1 : BT ? A3 : B2 + A3;
-    run_steps<A1 + B1, B2, A3, LEFT0, A3>(
-        steps,
-        [&](auto half, int buf) {
-            constexpr int h = decltype(half)::value;
-            const uint8_t* p = lds + buf * A_BYTES;
+    const auto read_a = [&](auto half, int buf) {
+        constexpr int h = decltype(half)::value;
+        const uint8_t* p = lds + buf * A_BYTES;
 #pragma unroll
-            for (int i = 0; i < MH; ++i) av[i].read(p, a_at + (h * 2 * MH + i) * 2048);
+        for (int i = 0; i < MH; ++i) av[i].read(p, a_at + (h * 2 * MH + i) * 2048);
+        if constexpr (MX) {
+            const uint8_t* sp = lds + read_step / kScaleSteps % 2 * SCALE_BUF + read_step % kScaleSteps * 4;
+#pragma unroll
+            for (int i = 0; i < MH; ++i) a_scale[i] = sp[a_scale_at + (h * 2 * MH + i) * 16 * kScalePiece];
+            read_step += h;
+        }
+    };
+    const auto read_b = [&](auto half, int buf) {
+        constexpr int h = decltype(half)::value;
+        const uint8_t* p = lds + buf * kBBytes;
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            if constexpr (BT)
+                bv[h][j].read(p, b_at ^ (h * 8 + wn * 2 + j) * 32);
+            else
+                bv[h][j].read(p, b_at + (h * 8 + j) * 2048);
+        }
+        if constexpr (MX) {
+            const uint8_t* sp = lds + read_step / kScaleSteps % 2 * SCALE_BUF + read_step % kScaleSteps * 4;
+#pragma unroll
+            for (int j = 0; j < 2; ++j) b_scale[h][j] = sp[b_scale_at + (h * 8 + j) * 16 * kScalePiece];
+        }
+    };
+    const auto multiply = [&](auto half_a, auto half_b) {
+        constexpr int ha = decltype(half_a)::value, hb = decltype(half_b)::value;
+        if constexpr (MX) {
+#pragma unroll
+            for (int i = 0; i < MH; ++i)
+#pragma unroll
+                for (int j = 0; j < 2; ++j)
+                    acc[ha][i][hb * 2 + j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
+                        bv[hb][j].whole(), av[i].whole(), acc[ha][i][hb * 2 + j], 0, 0, 0, b_scale[hb][j], 0,
+                        a_scale[i]);
+        } else {
+#pragma unroll
+            for (int i = 0; i < MH; ++i)
+#pragma unroll
+                for (int j = 0; j < 2; ++j)
+                    acc[ha][i][hb * 2 + j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+                        bv[hb][j].template half<0>(), av[i].template half<0>(), acc[ha][i][hb * 2 + j], 0, 0, 0);
+#pragma unroll
+            for (int i = 0; i < MH; ++i)
+#pragma unroll
+                for (int j = 0; j < 2; ++j)
+                    acc[ha][i][hb * 2 + j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+                        bv[hb][j].template half<1>(), av[i].template half<1>(), acc[ha][i][hb * 2 + j], 0, 0, 0);
+        }
+    };
+    const auto load = [&](auto quarter, int step, int buf) {
+        constexpr int q = decltype(quarter)::value;
+        uint8_t* pa = lds + buf * A_BYTES;
+        uint8_t* pb = lds + B_AT + buf * kBBytes;
+        if constexpr (q == 1) {
             if constexpr (MX) {
-                const uint8_t* sp = lds + read_step / kScaleSteps % 2 * SCALE_BUF + read_step % kScaleSteps * 4;
-#pragma unroll
-                for (int i = 0; i < MH; ++i) a_scale[i] = sp[a_scale_at + (h * 2 * MH + i) * 16 * kScalePiece];
-                read_step += h;
+                if (step % kScaleSteps == 0) load_scales(step);
             }
-        },
-        [&](auto half, int buf) {
-            constexpr int h = decltype(half)::value;
-            const uint8_t* p = lds + buf * kBBytes;
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                if constexpr (BT)
-                    bv[h][j].read(p, b_at ^ (h * 8 + wn * 2 + j) * 32);
-                else
-                    bv[h][j].read(p, b_at + (h * 8 + j) * 2048);
-            }
-            if constexpr (MX) {
-                const uint8_t* sp = lds + read_step / kScaleSteps % 2 * SCALE_BUF + read_step % kScaleSteps * 4;
-#pragma unroll
-                for (int j = 0; j < 2; ++j) b_scale[h][j] = sp[b_scale_at + (h * 8 + j) * 16 * kScalePiece];
-            }
-        },
-        [&](auto half_a, auto half_b) {
-            constexpr int ha = decltype(half_a)::value, hb = decltype(half_b)::value;
-            if constexpr (MX) {
-#pragma unroll
-                for (int i = 0; i < MH; ++i)
-#pragma unroll
-                    for (int j = 0; j < 2; ++j)
-                        acc[ha][i][hb * 2 + j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
-                            bv[hb][j].whole(), av[i].whole(), acc[ha][i][hb * 2 + j], 0, 0, 0, b_scale[hb][j], 0,
-                            a_scale[i]);
-            } else {
-#pragma unroll
-                for (int i = 0; i < MH; ++i)
-#pragma unroll
-                    for (int j = 0; j < 2; ++j)
-                        acc[ha][i][hb * 2 + j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
-                            bv[hb][j].template half<0>(), av[i].template half<0>(), acc[ha][i][hb * 2 + j], 0, 0, 0);
-#pragma unroll
-                for (int i = 0; i < MH; ++i)
-#pragma unroll
-                    for (int j = 0; j < 2; ++j)
-                        acc[ha][i][hb * 2 + j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
-                            bv[hb][j].template half<1>(), av[i].template half<1>(), acc[ha][i][hb * 2 + j], 0, 0, 0);
-            }
-        },
-        [&](auto quarter, int step, int buf) {
-            constexpr int q = decltype(quarter)::value;
-            uint8_t* pa = lds + buf * A_BYTES;
-            uint8_t* pb = lds + B_AT + buf * kBBytes;
-            if constexpr (q == 1) {
-                if constexpr (MX) {
-                    if (step % kScaleSteps == 0) load_scales(step);
-                }
-                a.template load<0, A1>(a_buf, step, pa);
-                if constexpr (!BT) br.template load<0, 2>(b_buf[0], step, pb);
-            } else if constexpr (q == 2) {
-                if constexpr (BT)
-                    bc.load(step, pb);
-                else
-                    br.template load<0, 2>(b_buf[1], step, pb + kBBytes / 2);
-            } else {
-                a.template load<A1, MH>(a_buf, step, pa + A1 * 64 * kStepBytes);
-            }
-        });
+            a.template load<0, A1>(a_buf, step, pa);
+            if constexpr (!BT) br.template load<0, 2>(b_buf[0], step, pb);
+        } else if constexpr (q == 2) {
+            if constexpr (BT)
+                bc.load(step, pb);
+            else
+                br.template load<0, 2>(b_buf[1], step, pb + kBBytes / 2);
+        } else {
+            a.template load<A1, MH>(a_buf, step, pa + A1 * 64 * kStepBytes);
+        }
+    };
+    if constexpr (SHORT) {
+        constexpr std::integral_constant<int, 0> h0{};
+        constexpr std::integral_constant<int, 1> h1{};
+        run_short_steps<STAGES, MH + 4>(
+            steps,
+            [&](int buf) {
+                read_b(h0, buf);
+                read_b(h1, buf);
+                read_a(h0, buf);
+                multiply(h0, h0);
+                multiply(h0, h1);
+                read_a(h1, buf);
+                multiply(h1, h0);
+                multiply(h1, h1);
+            },
+            [&](int step, int buf) {
+                load(h1, step, buf);
+                load(std::integral_constant<int, 2>{}, step, buf);
+                load(std::integral_constant<int, 3>{}, step, buf);
+            });
+    } else {
+        run_steps<A1 + B1, B2, A3, LEFT0, A3>(steps, read_a, read_b, multiply, load);
+    }
 
     // epilogue: eight columns of one row a lane, of two tiles of 16, once behind SwiGLU
     // and twice without.  Bias and residual are all asked for before the first use: one
