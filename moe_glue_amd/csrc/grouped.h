@@ -77,15 +77,19 @@ struct Tile {
 // L2, and an expert with many rows is not one XCD's alone (64 experts under skewed
 // routing, MXFP8: 187 us with an eighth of all tiles at a stretch, 171 so).  Every wave
 // looks for itself: a lane sums the tiles of up to 8 experts and the wave's prefix sums
-// find the lane that holds the tile; then its experts, one a lane, the same way.
+// find the lane that holds the tile; then, past 64 experts, the lane's own the same way.
 constexpr int kTogether = 8, kRun = 8;
 __device__ __forceinline__ Tile find_tile(const GroupedRows& g, int col_tiles, int whole) {
     const int lane = (int)(threadIdx.x % kWave);
     const int per = (g.E + kWave - 1) / kWave;
     int mine = 0;
+    Segment s = {0, 0};
     for (int i = 0; i < per; ++i) {
         const int e = lane * per + i;
-        if (e < g.E) mine += row_tiles(segment(g, e).n, whole);
+        if (e < g.E) {
+            s = segment(g, e);
+            mine += row_tiles(s.n, whole);
+        }
     }
     const int upto = wave_inclusive_sum(mine);
     const int total = __builtin_amdgcn_readlane(upto, kWave - 1) * col_tiles;
@@ -95,10 +99,14 @@ __device__ __forceinline__ Tile find_tile(const GroupedRows& g, int col_tiles, i
     if (u >= total) return {0, 0, 0, 0};
     const int owner = __builtin_ctzll(__ballot(upto * col_tiles > u));
     const int before = __builtin_amdgcn_readlane(upto - mine, owner);
-    Segment s = {0, 0};
-    if (lane < per && owner * per + lane < g.E) s = segment(g, owner * per + lane);
-    const int here = row_tiles(s.n, whole), until = before + wave_inclusive_sum(here);
-    const int which = __builtin_ctzll(__ballot(until * col_tiles > u));
+    int which = owner, here = mine, until = upto;
+    if (per > 1) {
+        s = {0, 0};
+        if (lane < per && owner * per + lane < g.E) s = segment(g, owner * per + lane);
+        here = row_tiles(s.n, whole);
+        until = before + wave_inclusive_sum(here);
+        which = __builtin_ctzll(__ballot(until * col_tiles > u));
+    }
     const int n = __builtin_amdgcn_readlane(s.n, which), tiles = __builtin_amdgcn_readlane(here, which);
     const int v = u - __builtin_amdgcn_readlane(until - here, which) * col_tiles;
     const int group = v / (kTogether * col_tiles);
@@ -107,7 +115,7 @@ __device__ __forceinline__ Tile find_tile(const GroupedRows& g, int col_tiles, i
     const int m = group * kTogether + at % in_group;
     const int units = (n + 63) / 64, each = units / tiles, more = units % tiles;
     const int first = (m * each + min(m, more)) * 64;
-    return {owner * per + which, __builtin_amdgcn_readlane(s.first, which) + first,
+    return {per > 1 ? owner * per + which : owner, __builtin_amdgcn_readlane(s.first, which) + first,
             min((each + (m < more ? 1 : 0)) * 64, n - first), at / in_group};
 }
 
@@ -134,7 +142,7 @@ __device__ __forceinline__ BufferWords buffer_words(const void* p, int64_t bytes
 // 16 bytes (or a dword) a lane from byte lane + scalar of a buffer to LDS, the wave's one
 // behind the other.  In assembly, for behind the builtin the compiler takes a transposing
 // LDS read for one of what is in flight, whatever buffer it goes to, and waits for all
-// loads before it (grad_w of 128 experts, 1536 x 2048: 423 us, GRAD_US without).  There is
+// loads before it (dx of 32768 rows, 128 experts, 1536 x 2048: 336 us, 298 without).  There is
 // no register to write; waiting is the caller's (loads_done).  M0 holds the LDS address,
 // and the wait state is the one it asks for before a load to LDS; nothing else in these
 // kernels uses M0.

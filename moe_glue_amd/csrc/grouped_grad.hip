@@ -9,7 +9,7 @@
 // other's products, and nothing waits for a store.  (Workgroups that stay and take tile
 // after tile, their loads running on into the next: 397 us for 128 experts' 1536 x 2048 of
 // 256 rows, since loads behind a tile's stores cannot be waited for without them; here
-// GRAD_US.)  db is summed from the fragments of dy, in the first column tiles.  Every
+// 367.)  db is summed from the fragments of dy, in the first column tiles.  Every
 // expert's gradient is written, zeros for one without rows; a tile is one workgroup's, so
 // the sums run in one order.
 #include "grouped.h"
