@@ -471,8 +471,8 @@ typedef enum moe_act {
  * pre bf16 [R, N] or NULL, with MOE_ACT_SWIGLU alone; out bf16 [R, N] or [R, N/2].
  * K % 8 == 0, out's columns % 8 == 0; every bf16 pointer 16-byte aligned, offsets
  * and counts 4-byte.  1 <= E <= MOE_E_MAX; N, K <= MOE_GROUPED_WIDTH_MAX; at most
- * MOE_GROUPED_TILES_MAX tiles of 256 rows by 256 columns of w's rows: (R / 256 +
- * min(E, R)) * ceil(N / 256).  R = 0 is a no-op.  Errors: MOE_ERR_NULL,
+ * MOE_GROUPED_TILES_MAX tiles of 64 rows by 256 rows of w: (R / 64 + min(E, R)) *
+ * ceil(N / 256).  R = 0 is a no-op.  Errors: MOE_ERR_NULL,
  * MOE_ERR_SHAPE, MOE_ERR_ALIGN, MOE_ERR_UNSUPPORTED, MOE_ERR_HIP. */
 moe_status moe_grouped_linear(const uint16_t* x, int32_t R, const int32_t* expert_offsets,
                               const int32_t* expert_counts, const uint16_t* w, int32_t E, int32_t N, int32_t K,
@@ -509,11 +509,18 @@ moe_status moe_grouped_linear_grad_x(const uint16_t* dy, int32_t R, const int32_
  * An expert without rows gets zeros, also with R = 0.  dy bf16 [R, N]; x bf16
  * [R, K]; dw [E, N, K], bf16, or fp32 with dw_fp32 != 0; dbias fp32 [E, N].
  * N % 8 == 0 and K % 8 == 0; dy, x and dw 16-byte aligned, dbias 4-byte.  At most
- * MOE_GROUPED_TILES_MAX tiles of 128 by 128: E * ceil(N / 128) * ceil(K / 128).
- * The same call gives the same bits every time.  Errors as moe_grouped_linear. */
+ * MOE_GROUPED_TILES_MAX tiles of 128 rows by 256 columns of dw, for each expert and,
+ * where one may have many rows, for each piece of them.
+ * The workspace must hold moe_grouped_linear_grad_w_workspace_bytes(R, E, N, K) bytes
+ * (16-byte aligned): partial sums of experts whose rows are cut into pieces, with few
+ * tiles or few experts for the rows; 0 where none can be (and for invalid arguments),
+ * and then it may be NULL.  It needs no initialisation, and calls that can overlap on
+ * the device need one each.  The same call gives the same bits every time.  Errors as
+ * moe_grouped_linear, and MOE_ERR_WORKSPACE. */
+size_t moe_grouped_linear_grad_w_workspace_bytes(int32_t R, int32_t E, int32_t N, int32_t K);
 moe_status moe_grouped_linear_grad_w(const uint16_t* dy, const uint16_t* x, int32_t R, const int32_t* expert_offsets,
                                      const int32_t* expert_counts, int32_t E, int32_t N, int32_t K, int32_t dw_fp32,
-                                     void* dw, float* dbias, void* stream);
+                                     void* dw, float* dbias, void* workspace, size_t workspace_bytes, void* stream);
 
 /* ------------------------------------------- gradients of the other steps */
 

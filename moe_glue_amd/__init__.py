@@ -43,6 +43,7 @@ __all__ = ["route", "route_workspace_bytes", "alloc_route_outputs", "route_padde
            "rmsnorm", "rmsnorm_fp8", "rmsnorm_mxfp8", "decode_layer", "decode_layer_mxfp4",
            "decode_layer_workspace_bytes", "alloc_decode_outputs", "linear_mxfp4",
            "grouped_linear", "grouped_linear_mxfp8", "grouped_linear_grad_x", "grouped_linear_grad_w",
+           "grouped_linear_grad_w_workspace_bytes",
            "swiglu_backward", "combine_backward", "expand_rows_backward", "route_backward",
            "copy_probe", "mix_probe", "MoEGlueError", "MoEGlueArgumentError", "E_MAX", "K_MAX",
            "NORM_H_MAX", "DECODE_T_MAX"]
@@ -789,11 +790,18 @@ def grouped_linear_grad_x(dy, w, offsets=None, counts=None, out=None):
     return out
 
 
-def grouped_linear_grad_w(dy, x, offsets=None, counts=None, dtype=None, bias: bool = False, out=None, bias_out=None):
+def grouped_linear_grad_w_workspace_bytes(R: int, E: int, N: int, K: int) -> int:
+    return int(load().moe_grouped_linear_grad_w_workspace_bytes(R, E, N, K))
+
+
+def grouped_linear_grad_w(dy, x, offsets=None, counts=None, dtype=None, bias: bool = False, out=None, bias_out=None,
+                          workspace=None):
     """dw[e] = dy^T x over each expert's rows, and with `bias` (or `bias_out`) the
     column sums of dy: returns (dw [E, N, K] in `dtype`, bf16 (the default) or
-    fp32, dbias fp32 [E, N] or None); [N, K] and [N] without offsets.  See
-    moe_grouped_linear_grad_w in include/moe_glue.h."""
+    fp32, dbias fp32 [E, N] or None); [N, K] and [N] without offsets.  `workspace`: a
+    uint8 tensor of grouped_linear_grad_w_workspace_bytes(R, E, N, K) bytes, allocated
+    where it is needed and not given.  See moe_grouped_linear_grad_w in
+    include/moe_glue.h."""
     torch = _torch()
     _need_gpu("dy", dy, torch.bfloat16, 2)
     dev = dy.device
@@ -820,8 +828,16 @@ def grouped_linear_grad_w(dy, x, offsets=None, counts=None, dtype=None, bias: bo
         _check_shape("bias_out", bias_out, torch.float32, (*lead, N), dev)
     elif bias:
         bias_out = torch.empty((*lead, N), dtype=torch.float32, device=dev)
+    if workspace is None:
+        need = grouped_linear_grad_w_workspace_bytes(R, E, N, K)
+        if need:
+            workspace = torch.empty((need,), dtype=torch.uint8, device=dev)
+    else:
+        _need_gpu("workspace", workspace, torch.uint8)
+        _same_device([("workspace", workspace)], dev)
     _enqueue("moe_grouped_linear_grad_w", dev, _ptr(dy), _ptr(x), R, _ptr(offsets), _ptr(counts), E, N, K,
-             int(dtype == torch.float32), _ptr(out), _ptr(bias_out))
+             int(dtype == torch.float32), _ptr(out), _ptr(bias_out), _ptr(workspace),
+             0 if workspace is None else workspace.numel())
     return out, bias_out
 
 

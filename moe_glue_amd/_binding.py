@@ -26,7 +26,8 @@ EXPORTED = ("moe_route_workspace_bytes", "moe_route", "moe_route_padded_rows", "
             "moe_route_expand_fp8", "moe_route_expand_mxfp8", "moe_noalloc_scratch_bytes", "moe_route_expand_noalloc",
             "moe_swiglu", "moe_combine", "moe_rmsnorm", "moe_rmsnorm_fp8", "moe_rmsnorm_mxfp8",
             "moe_decode_layer_workspace_bytes", "moe_decode_layer", "moe_decode_layer_mxfp4", "moe_linear_mxfp4",
-            "moe_grouped_linear", "moe_grouped_linear_mxfp8", "moe_grouped_linear_grad_x", "moe_grouped_linear_grad_w",
+            "moe_grouped_linear", "moe_grouped_linear_mxfp8", "moe_grouped_linear_grad_x",
+            "moe_grouped_linear_grad_w_workspace_bytes", "moe_grouped_linear_grad_w",
             "moe_swiglu_backward", "moe_combine_backward", "moe_expand_rows_backward", "moe_route_backward",
             "moe_copy_probe", "moe_mix_probe",
             "moe_status_string", "moe_last_error")
@@ -121,12 +122,15 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
                                            _vp, _vp, ctypes.c_size_t, _vp]
     lib.moe_linear_mxfp4.restype = ctypes.c_int
     lib.moe_linear_mxfp4.argtypes = [_vp, _i32, _i32, _vp, _vp, _i32, _vp, _vp]
+    lib.moe_grouped_linear_grad_w_workspace_bytes.restype = ctypes.c_size_t
+    lib.moe_grouped_linear_grad_w_workspace_bytes.argtypes = [_i32, _i32, _i32, _i32]
     for name, args in {
         "moe_grouped_linear": [_vp, _i32, _vp, _vp, _vp, _i32, _i32, _i32, _vp, _i32, _vp, _vp, _vp, _vp],
         "moe_grouped_linear_mxfp8": [_vp, _vp, _i32, _vp, _vp, _vp, _vp, _i32, _i32, _i32, _vp, _i32, _vp, _vp, _vp,
                                      _vp],
         "moe_grouped_linear_grad_x": [_vp, _i32, _vp, _vp, _vp, _i32, _i32, _i32, _vp, _vp],
-        "moe_grouped_linear_grad_w": [_vp, _vp, _i32, _vp, _vp, _i32, _i32, _i32, _i32, _vp, _vp, _vp],
+        "moe_grouped_linear_grad_w": [_vp, _vp, _i32, _vp, _vp, _i32, _i32, _i32, _i32, _vp, _vp, _vp, ctypes.c_size_t,
+                                      _vp],
         "moe_swiglu_backward": [_vp, _vp, _i32, _i32, _vp, _vp, _vp],
         "moe_combine_backward": [_vp, _vp, _vp, _vp, _i32, _i32, _i32, _vp, _vp, _vp],
         "moe_expand_rows_backward": [_vp, _vp, _vp, _i32, _i32, _i32, _vp, _vp],

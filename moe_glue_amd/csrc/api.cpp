@@ -729,6 +729,13 @@ moe_status check_grouped_width(const char* fn, const char* name, int32_t width, 
     return MOE_OK;
 }
 
+moe_status check_grad_w(const char* fn, const moe::GroupedRows& rows, int32_t N, int32_t K) {
+    moe_status s = check_grouped_width(fn, "K", K, 8);
+    if (s == MOE_OK) s = check_grouped_width(fn, "N", N, 8);
+    if (s != MOE_OK) return s;
+    return check_grouped(fn, rows, N, K, moe::grouped_grad_w_tiles(rows, N, K));
+}
+
 moe_status grouped_impl(const char* fn, const moe::GroupedArgs& g, bool mx, int act, void* stream) {
     if (act != MOE_ACT_NONE && act != MOE_ACT_SWIGLU) return fail(MOE_ERR_UNSUPPORTED, "%s: act=%d", fn, act);
     const bool swiglu = act == MOE_ACT_SWIGLU;
@@ -790,21 +797,32 @@ moe_status moe_grouped_linear_grad_x(const uint16_t* dy, int32_t R, const int32_
                     fn);
 }
 
+size_t moe_grouped_linear_grad_w_workspace_bytes(int32_t R, int32_t E, int32_t N, int32_t K) {
+    const char* fn = "moe_grouped_linear_grad_w_workspace_bytes";
+    const int32_t some = 0;  // (segments or none: E may be any)
+    if (check_grad_w(fn, {&some, nullptr, E, R}, N, K) != MOE_OK) return 0;
+    return moe::grouped_grad_w_workspace_bytes({nullptr, nullptr, E, R}, N, K);
+}
+
 moe_status moe_grouped_linear_grad_w(const uint16_t* dy, const uint16_t* x, int32_t R, const int32_t* expert_offsets,
                                      const int32_t* expert_counts, int32_t E, int32_t N, int32_t K, int32_t dw_fp32,
-                                     void* dw, float* dbias, void* stream) {
+                                     void* dw, float* dbias, void* workspace, size_t workspace_bytes, void* stream) {
     const char* fn = "moe_grouped_linear_grad_w";
     const moe::GroupedRows rows = {expert_offsets, expert_counts, E, R};
-    moe_status s = check_grouped_width(fn, "K", K, 8);
-    if (s == MOE_OK) s = check_grouped_width(fn, "N", N, 8);
-    if (s == MOE_OK) s = check_grouped(fn, rows, N, K, moe::grouped_grad_w_tiles(E, N, K));
+    const moe_status s = check_grad_w(fn, rows, N, K);
     if (s != MOE_OK) return s;
     if (!dw || (R > 0 && (!dy || !x))) return fail(MOE_ERR_NULL, "%s: NULL tensor pointer", fn);
     if (!aligned16(dy) || !aligned16(x) || !aligned16(dw))
         return fail(MOE_ERR_ALIGN, "%s: dy, x and dw must be 16-byte aligned", fn);
     if (!aligned4(dbias)) return fail(MOE_ERR_ALIGN, "%s: dbias must be 4-byte aligned", fn);
-    return from_hip(moe::launch_grouped_grad_w({rows, dy, x, N, K, dw, dw_fp32 != 0, dbias},
-                                               static_cast<hipStream_t>(stream)),
+    const size_t need = moe::grouped_grad_w_workspace_bytes(rows, N, K);
+    if (need > 0 && (workspace == nullptr || workspace_bytes < need))
+        return fail(MOE_ERR_WORKSPACE, "%s: workspace of %zu bytes needed, %zu given%s", fn, need, workspace_bytes,
+                    workspace ? "" : " (NULL)");
+    if (need > 0 && !aligned16(workspace))
+        return fail(MOE_ERR_WORKSPACE, "%s: workspace must be 16-byte aligned", fn);
+    return from_hip(moe::launch_grouped_grad_w({rows, dy, x, N, K, dw, dw_fp32 != 0, dbias, 0, 0, nullptr, nullptr},
+                                               workspace, static_cast<hipStream_t>(stream)),
                     fn);
 }
 

@@ -30,17 +30,72 @@ constexpr int kStages = 3;
 constexpr int kLoads = AOperand::LOADS + BOperand::LOADS;
 static_assert(2 * kStages * kStage <= kLdsBytes, "two workgroups a CU");
 
-template <bool WIDE, bool DB>
+// Pieces of an expert's n rows, of up to `piece`; none has one too.
+__device__ __forceinline__ int pieces_of(int n, int piece) { return max((n + piece - 1) / piece, 1); }
+
+// A piece of an expert, of `of`; the slots of the partial sums are numbered over the
+// experts that have several pieces, and slot is the expert's first.
+struct Piece {
+    int e, at;  // e = -1: none
+    int of, slot;
+};
+// Every expert's first piece has a workgroup a tile of its own; these are the others:
+// number u of them, as find_tile() finds its tile.
+__device__ __forceinline__ Piece find_piece(const GroupedRows& g, int piece, int u) {
+    const int lane = (int)(threadIdx.x % kWave);
+    int before = 0, slots = 0;
+    for (int e0 = 0; e0 < g.E; e0 += kWave) {
+        const int here = e0 + lane < g.E ? pieces_of(segment(g, e0 + lane).n, piece) : 1;
+        const int upto = before + wave_inclusive_sum(here - 1);
+        const int slots_upto = slots + wave_inclusive_sum(here > 1 ? here : 0);
+        const int last = __builtin_amdgcn_readlane(upto, kWave - 1);
+        if (u < last) {
+            const int which = __builtin_ctzll(__ballot(upto > u));
+            const int of = __builtin_amdgcn_readlane(here, which);
+            return {e0 + which, u - (__builtin_amdgcn_readlane(upto, which) - (of - 1)) + 1, of,
+                    __builtin_amdgcn_readlane(slots_upto, which) - of};
+        }
+        before = last;
+        slots = __builtin_amdgcn_readlane(slots_upto, kWave - 1);
+    }
+    return {-1, 0, 0, 0};
+}
+// The first slot of expert e.
+__device__ __forceinline__ int slot_of(const GroupedRows& g, int piece, int e) {
+    int slots = 0;
+    for (int e0 = 0; e0 < e; e0 += kWave) {
+        const int at = e0 + (int)(threadIdx.x % kWave);
+        const int here = at < e ? pieces_of(segment(g, at).n, piece) : 1;
+        slots += __builtin_amdgcn_readlane(wave_inclusive_sum(here > 1 ? here : 0), kWave - 1);
+    }
+    return slots;
+}
+
+template <bool WIDE, bool DB, bool PIECES>
 __global__ __launch_bounds__(kThreads, 2) void grad_w_kernel(GroupedGradArgs g, int k_tiles, int per_expert) {
     __shared__ __align__(16) uint8_t lds[kStages * kStage];
     const int lane = (int)(threadIdx.x % kWave), wave = (int)uniform(threadIdx.x / kWave);
     const int wm = wave / 2, wn = wave % 2;
-    // Tiles expert by expert, row by row: each XCD has a share of every expert, so that
-    // none waits for the one that has most rows (64 experts, skewed: 833 us with whole
-    // experts on an XCD, and no less for 128 even ones).
-    const int e = (int)(blockIdx.x / (uint32_t)per_expert), at = (int)(blockIdx.x % (uint32_t)per_expert);
+    // Tiles expert by expert (piece by piece), row by row: each XCD has a share of every
+    // expert, so that none waits for the one that has most rows (64 experts, skewed: 833
+    // us with whole experts on an XCD, and no less for 128 even ones).
+    Piece p = {(int)(blockIdx.x / (uint32_t)per_expert), 0, 1, 0};
+    if constexpr (PIECES) {
+        if (p.e >= g.rows.E) {
+            p = find_piece(g.rows, g.piece, p.e - g.rows.E);
+        } else {
+            p.of = pieces_of(segment(g.rows, p.e).n, g.piece);
+            if (p.of > 1) p.slot = slot_of(g.rows, g.piece, p.e);
+        }
+        if (p.e < 0 || (p.of > 1 && p.slot + p.of > g.slots)) return;  // (the latter if segments overlap)
+    }
+    const int e = p.e, at = (int)(blockIdx.x % (uint32_t)per_expert);
     const int n0 = at / k_tiles * kTileN, k0 = at % k_tiles * kTileK;
-    const Segment seg = segment(g.rows, e);
+    Segment seg = segment(g.rows, e);
+    if constexpr (PIECES) {
+        seg.first += p.at * g.piece;
+        seg.n = min(seg.n - p.at * g.piece, g.piece);
+    }
     const uint32_t lda = (uint32_t)g.N * 2, ldb = (uint32_t)g.K * 2;
     const int steps = (seg.n + kStep - 1) / kStep;
     AOperand a;
@@ -112,12 +167,15 @@ __global__ __launch_bounds__(kThreads, 2) void grad_w_kernel(GroupedGradArgs g, 
         buf = buf == 2 ? 0 : buf + 1;
     }
 
+    const bool partial = PIECES && p.of > 1;
+    float* const sums_out = partial ? g.partial_db + (int64_t)(p.slot + p.at) * g.N : DB ? g.db + (int64_t)e * g.N : nullptr;
+    const int64_t first = (int64_t)(partial ? p.slot + p.at : e) * g.N * g.K;
 #pragma unroll
     for (int i = 0; i < MT; ++i) {
         const int n = n0 + (wm * MT + i) * 16 + lane % 16;
         if (sum_here) {  // a lane has summed its quarter of the rows
             const float s = __builtin_bit_cast(float, across_rows(__builtin_bit_cast(uint32_t, sums[i])));
-            if (lane < 16 && n < g.N) g.db[(int64_t)e * g.N + n] = s;
+            if (lane < 16 && n < g.N) sums_out[n] = s;
         }
 #pragma unroll
         for (int j = 0; j < NT; j += 2) {
@@ -125,9 +183,9 @@ __global__ __launch_bounds__(kThreads, 2) void grad_w_kernel(GroupedGradArgs g, 
             float v[8];
             pair_values(acc[i][j], acc[i][j + 1], v);
             if (n < g.N && k < g.K) {
-                const int64_t o = ((int64_t)e * g.N + n) * g.K + k;
-                if constexpr (WIDE) {
-                    f32x4* d = reinterpret_cast<f32x4*>(static_cast<float*>(g.dw) + o);
+                const int64_t o = first + (int64_t)n * g.K + k;
+                if (WIDE || partial) {
+                    f32x4* d = reinterpret_cast<f32x4*>((partial ? g.partial : static_cast<float*>(g.dw)) + o);
                     d[0] = f32x4{v[0], v[1], v[2], v[3]};
                     d[1] = f32x4{v[4], v[5], v[6], v[7]};
                 } else {
@@ -138,24 +196,115 @@ __global__ __launch_bounds__(kThreads, 2) void grad_w_kernel(GroupedGradArgs g, 
     }
 }
 
-}  // namespace
-
-int64_t grouped_grad_w_tiles(int E, int N, int K) {
-    return (int64_t)E * ((N + kTileN - 1) / kTileN) * ((K + kTileK - 1) / kTileK);
+// The partial sums of the experts that have several: workgroup row y is the y-th of
+// them, x a share of its N K values and of its N sums.
+template <bool WIDE, bool DB>
+__global__ __launch_bounds__(kThreads) void join_kernel(GroupedGradArgs g, uint32_t vectors) {
+    // the blockIdx.y-th expert with several pieces, and its slot
+    const int lane = (int)(threadIdx.x % kWave);
+    int e = -1, of = 0, slot = 0, seen = 0, slots = 0;
+    for (int e0 = 0; e0 < g.rows.E; e0 += kWave) {
+        const int here = e0 + lane < g.rows.E ? pieces_of(segment(g.rows, e0 + lane).n, g.piece) : 0;
+        const int several = here > 1 ? here : 0;
+        const int upto = seen + wave_inclusive_sum(several > 0 ? 1 : 0), slots_upto = slots + wave_inclusive_sum(several);
+        const uint64_t which = __ballot(several > 0 && upto == (int)blockIdx.y + 1);
+        if (which != 0) {
+            const int w = __builtin_ctzll(which);
+            e = e0 + w;
+            of = __builtin_amdgcn_readlane(several, w);
+            slot = __builtin_amdgcn_readlane(slots_upto - several, w);
+        }
+        seen = __builtin_amdgcn_readlane(upto, kWave - 1);
+        slots = __builtin_amdgcn_readlane(slots_upto, kWave - 1);
+    }
+    if (e < 0 || slot + of > g.slots) return;
+    const int64_t size = (int64_t)g.N * g.K;
+    for (uint32_t i = blockIdx.x * kThreads + threadIdx.x; i < vectors; i += gridDim.x * kThreads) {
+        float v[8] = {};
+        for (int q = 0; q < of; ++q) {
+            const f32x4* s = reinterpret_cast<const f32x4*>(g.partial + (slot + q) * size) + (size_t)i * 2;
+            const f32x4 a = s[0], b = s[1];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                v[j] += a[j];
+                v[4 + j] += b[j];
+            }
+        }
+        if constexpr (WIDE) {
+            f32x4* d = reinterpret_cast<f32x4*>(static_cast<float*>(g.dw) + e * size) + (size_t)i * 2;
+            d[0] = f32x4{v[0], v[1], v[2], v[3]};
+            d[1] = f32x4{v[4], v[5], v[6], v[7]};
+        } else {
+            reinterpret_cast<u32x4*>(static_cast<uint16_t*>(g.dw) + e * size)[i] = pack8(v);
+        }
+    }
+    if constexpr (DB) {
+        for (int n = (int)(blockIdx.x * kThreads + threadIdx.x); n < g.N; n += (int)(gridDim.x * kThreads)) {
+            float v = 0.0f;
+            for (int q = 0; q < of; ++q) v += g.partial_db[(int64_t)(slot + q) * g.N + n];
+            g.db[(int64_t)e * g.N + n] = v;
+        }
+    }
 }
 
-hipError_t launch_grouped_grad_w(const GroupedGradArgs& g, hipStream_t stream) {
+template <bool WIDE, bool DB>
+hipError_t launch(const GroupedGradArgs& g, hipStream_t stream) {
     const int k_tiles = (g.K + kTileK - 1) / kTileK, per_expert = (g.N + kTileN - 1) / kTileN * k_tiles;
-    const uint32_t grid = (uint32_t)g.rows.E * (uint32_t)per_expert;
-    if (g.wide && g.db)
-        grad_w_kernel<true, true><<<grid, kThreads, 0, stream>>>(g, k_tiles, per_expert);
-    else if (g.wide)
-        grad_w_kernel<true, false><<<grid, kThreads, 0, stream>>>(g, k_tiles, per_expert);
-    else if (g.db)
-        grad_w_kernel<false, true><<<grid, kThreads, 0, stream>>>(g, k_tiles, per_expert);
-    else
-        grad_w_kernel<false, false><<<grid, kThreads, 0, stream>>>(g, k_tiles, per_expert);
+    if (g.piece == 0) {
+        grad_w_kernel<WIDE, DB, false>
+            <<<(uint32_t)g.rows.E * (uint32_t)per_expert, kThreads, 0, stream>>>(g, k_tiles, per_expert);
+        return hipGetLastError();
+    }
+    const int pieces = g.rows.R / g.piece + g.rows.E;
+    grad_w_kernel<WIDE, DB, true>
+        <<<(uint32_t)pieces * (uint32_t)per_expert, kThreads, 0, stream>>>(g, k_tiles, per_expert);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    const uint32_t vectors = (uint32_t)((int64_t)g.N * g.K / 8);
+    const uint32_t experts = (uint32_t)(g.rows.R / g.piece < g.rows.E ? g.rows.R / g.piece : g.rows.E);
+    const uint32_t blocks = (vectors + kThreads - 1) / kThreads;
+    join_kernel<WIDE, DB><<<dim3(blocks < 256 ? blocks : 256, experts), kThreads, 0, stream>>>(g, vectors);
     return hipGetLastError();
+}
+
+// Rows of a piece: those whose steps are as many as one of the workgroups that run at a
+// time would have if all tiles' steps were spread evenly, 1024 at least: below that
+// joining costs more than it gives.  0: whole experts, where none can have more rows, or
+// an expert's tiles are many enough to be busy alone.  (34 skewed experts of 31239 rows,
+// 784 x 328 in fp32: 369 us whole, 79 in pieces; one of 3059 rows, 224 x 4232, with dx: 79
+// and 47.  But 128 even experts of 32768 rows, 1536 x 2048, 96 tiles each: 367 and 386.)
+constexpr int kSlots = 512, kPieceMin = 1024, kTilesMax = 64;
+int piece_rows(const GroupedRows& g, int N, int K) {
+    const int64_t per_expert = (int64_t)((N + kTileN - 1) / kTileN) * ((K + kTileK - 1) / kTileK);
+    if (per_expert >= kTilesMax) return 0;
+    int64_t rows = (g.R * per_expert + kSlots - 1) / kSlots;
+    rows = ((rows < kPieceMin ? kPieceMin : rows) + kStep - 1) / kStep * kStep;
+    return rows >= g.R ? 0 : (int)rows;
+}
+// Partial sums: experts with several pieces have more than a piece's rows each, and at
+// most twice as many pieces as whole ones.
+int64_t slots_of(const GroupedRows& g, int piece) { return piece == 0 ? 0 : 2 * (int64_t)(g.R / piece); }
+
+}  // namespace
+
+int64_t grouped_grad_w_tiles(const GroupedRows& g, int N, int K) {
+    const int64_t per_expert = (int64_t)((N + kTileN - 1) / kTileN) * ((K + kTileK - 1) / kTileK);
+    if (g.R < 0 || g.E < 1) return 0;
+    const int piece = piece_rows(g, N, K);
+    return (g.E + (piece > 0 ? g.R / piece : 0)) * per_expert;
+}
+
+size_t grouped_grad_w_workspace_bytes(const GroupedRows& g, int N, int K) {
+    return (size_t)slots_of(g, piece_rows(g, N, K)) * N * (K + 1) * sizeof(float);
+}
+
+hipError_t launch_grouped_grad_w(GroupedGradArgs g, void* workspace, hipStream_t stream) {
+    g.piece = piece_rows(g.rows, g.N, g.K);
+    g.slots = (int)slots_of(g.rows, g.piece);
+    g.partial = static_cast<float*>(workspace);
+    g.partial_db = g.partial + (int64_t)g.slots * g.N * g.K;
+    if (g.wide) return g.db ? launch<true, true>(g, stream) : launch<true, false>(g, stream);
+    return g.db ? launch<false, true>(g, stream) : launch<false, false>(g, stream);
 }
 
 }  // namespace moe

@@ -298,9 +298,13 @@ struct GroupedGradArgs {
     void* dw;            // bf16 or fp32 [E, N, K]
     bool wide;           // dw in fp32
     float* db;           // fp32 [E, N] or null
+    int piece, slots;    // (set by the launch) rows of a piece, 0: whole experts; partial sums
+    float* partial;      // partial sums [pieces, N, K] and [pieces, N]
+    float* partial_db;
 };
-int64_t grouped_grad_w_tiles(int E, int N, int K);
-hipError_t launch_grouped_grad_w(const GroupedGradArgs& g, hipStream_t stream);
+int64_t grouped_grad_w_tiles(const GroupedRows& rows, int N, int K);
+size_t grouped_grad_w_workspace_bytes(const GroupedRows& rows, int N, int K);
+hipError_t launch_grouped_grad_w(GroupedGradArgs g, void* workspace, hipStream_t stream);
 
 // ------------------------------------------- gradients of the streaming steps
 hipError_t launch_swiglu_backward(const void* h, const void* dact, int R, int I, void* dh, void* act,
