@@ -21,7 +21,7 @@ BUILD = os.path.join(ROOT, "_build")
 
 SOURCES = ["api.cpp", "route.hip", "dispatch.hip", "expand.hip", "quant.hip", "swiglu.hip", "combine.hip",
            "probe.hip", "noalloc.hip", "place_expand.hip", "norm.hip", "decode_layer.hip", "linear.hip",
-           "grouped_linear.hip", "grouped_grad.hip", "grads.hip"]
+           "grouped_linear.hip", "grouped_few.hip", "grouped_grad.hip", "grads.hip"]
 HEADERS = ["device_common.h", "kernels.h", "route_common.h", "fp8_common.h", "place_copy.h", "mfma_rows.h",
            "grouped.h"]
 ARCH = "gfx950"

@@ -394,4 +394,24 @@ __device__ __forceinline__ int pair_column() {
     return q % 2 * 16 + q / 2 * 8;
 }
 
+// ---------------------------------------------------------------- epilogue
+// silu(g) u in fp32, as moe_swiglu has it.
+__device__ __forceinline__ float silu_mul(float g, float u) {
+    const float e = __builtin_amdgcn_exp2f(-g * 1.4426950408889634f);
+    return g * __builtin_amdgcn_rcpf(1.0f + e) * u;
+}
+
+__device__ __forceinline__ u32x4 load8(const uint16_t* p) { return *reinterpret_cast<const u32x4*>(p); }
+__device__ __forceinline__ void add8(float (&v)[8], const u32x4& b) {
+    float w[8];
+    unpack8(b, w);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] += w[i];
+}
+__device__ __forceinline__ void store8(uint16_t* p, const float (&v)[8]) { *reinterpret_cast<u32x4*>(p) = pack8(v); }
+
+constexpr int kCus = 256;
+// Workgroups for so many tiles: whole turns of find_tile's.
+inline uint32_t grouped_grid(int64_t tiles) { return (uint32_t)((tiles + 8 * kRun - 1) / (8 * kRun) * (8 * kRun)); }
+
 }  // namespace moe

@@ -14,21 +14,6 @@ constexpr int kScaleSteps = 4;   // those of so many steps
 constexpr int kBBytes = kCols * kStepBytes;
 constexpr int kShortMH = 1;      // tiles of up to 64 of these rows take the short steps
 
-// silu(g) u in fp32, as moe_swiglu has it.
-__device__ __forceinline__ float silu_mul(float g, float u) {
-    const float e = __builtin_amdgcn_exp2f(-g * 1.4426950408889634f);
-    return g * __builtin_amdgcn_rcpf(1.0f + e) * u;
-}
-
-__device__ __forceinline__ u32x4 load8(const uint16_t* p) { return *reinterpret_cast<const u32x4*>(p); }
-__device__ __forceinline__ void add8(float (&v)[8], const u32x4& b) {
-    float w[8];
-    unpack8(b, w);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] += w[i];
-}
-__device__ __forceinline__ void store8(uint16_t* p, const float (&v)[8]) { *reinterpret_cast<u32x4*>(p) = pack8(v); }
-
 // A piece of the scale bytes of 16 LDS rows into LDS, a dword a lane: lane l has
 // bytes 4 (l % 4) .. + 3 of the row of scales that starts at byte `row` from base on.
 __device__ __forceinline__ void load_scale_piece(const uint8_t* base, int64_t bytes, uint32_t row, int piece, uint32_t ld,
@@ -302,20 +287,26 @@ __global__ __launch_bounds__(kGroupedThreads, 2) void grouped_kernel(GroupedArgs
         product<1, BT, MX, SWIGLU>(g, t, lds);
 }
 
-constexpr int kCus = 256;
+// From so many tiles of 64 rows by 256 columns on those keep enough CUs at work.  Dense, 512 x
+// 1024 x 7168 (32 tiles): 63 us with them, 23 in grouped_few.hip; 64 tiles (8 experts, 1024 x 1024 x
+// 2048): 23.4 and 22.0, MXFP8 17.9 and 20.9; 88 (512 x 2816 x 2048): 24.0 and 25.8.
+constexpr int kFewTiles = 64;
 
 template <bool BT, bool MX, bool SWIGLU>
 hipError_t launch(const GroupedArgs& g, hipStream_t stream) {
     const int cols = SWIGLU ? kCols / 2 : kCols, out_cols = SWIGLU ? g.N / 2 : g.N;
     const int col_tiles = (out_cols + cols - 1) / cols;
-    // Fewer rows a tile where whole ones would leave CUs without work; rows spread
-    // evenly over the experts, as far as the host can know.
+    // Rows spread evenly over the experts, as far as the host can know.
     const int experts = g.rows.E < g.rows.R ? g.rows.E : g.rows.R;
+    const auto tiles = [&](int whole) {
+        return (int64_t)experts * ((g.rows.R / experts + whole - 1) / whole) * col_tiles;
+    };
+    if (tiles(64) < kFewTiles) return launch_grouped_few(g, BT, SWIGLU, tiles(64), stream);
+    // Fewer rows a tile where whole ones would leave CUs without work.
     int whole = kRows;
-    while (whole > 64 && (int64_t)experts * ((g.rows.R / experts + whole - 1) / whole) * col_tiles < kCus) whole /= 2;
-    const int64_t tiles = grouped_tiles(g.rows, whole, col_tiles);
-    const uint32_t grid = (uint32_t)((tiles + 8 * kRun - 1) / (8 * kRun) * (8 * kRun));  // whole turns
-    grouped_kernel<BT, MX, SWIGLU><<<grid, kGroupedThreads, 0, stream>>>(g, col_tiles, whole);
+    while (whole > 64 && tiles(whole) < kCus) whole /= 2;
+    grouped_kernel<BT, MX, SWIGLU><<<grouped_grid(grouped_tiles(g.rows, whole, col_tiles)), kGroupedThreads, 0, stream>>>(
+        g, col_tiles, whole);
     return hipGetLastError();
 }
 

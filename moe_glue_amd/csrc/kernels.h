@@ -290,6 +290,8 @@ struct GroupedArgs {
 int64_t grouped_linear_tiles(const GroupedRows& rows, int cols);
 hipError_t launch_grouped_linear(const GroupedArgs& g, bool swiglu, hipStream_t stream);
 hipError_t launch_grouped_grad_x(const GroupedArgs& g, hipStream_t stream);
+// Either of them (transposed: grad_x) where tiles of 64 rows by 256 columns are as few as `tiles`.
+hipError_t launch_grouped_few(const GroupedArgs& g, bool transposed, bool swiglu, int64_t tiles, hipStream_t stream);
 struct GroupedGradArgs {
     GroupedRows rows;
     const uint16_t* dy;  // bf16 [R, N]

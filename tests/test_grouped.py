@@ -45,7 +45,8 @@ def poison(t, segs, value=float("nan")):
 # rows: none, one, round 64, 128, 192, 256 and 320, several tiles, and more than four
 RAGGED = [[0, 1, 63, 0, 64, 65], [127, 128, 129, 0], [192, 193, 255, 256, 257], [0, 0, 319, 320, 321, 1], [1100, 0, 3],
           [1], [0]]
-WIDTHS = [(16, 8), (64, 72), (136, 64), (264, 128), (512, 136), (528, 264)]
+# (the last three: enough columns for the larger tiles)
+WIDTHS = [(16, 8), (64, 72), (136, 64), (264, 128), (512, 136), (528, 264), (4104, 72), (11016, 64), (11024, 136)]
 
 
 @pytest.mark.parametrize("act", [None, "swiglu"])
@@ -82,7 +83,7 @@ def test_linear(dev, case, act):
             assert (pre[dead] == SENTINEL).all()
 
 
-@pytest.mark.parametrize("R,N,K", [(1, 8, 8), (7, 24, 4096), (64, 256, 128), (65, 264, 192), (200, 1032, 520),
+@pytest.mark.parametrize("R,N,K", [(1, 8, 8), (7, 24, 4096), (16, 512, 1096), (17, 520, 640), (33, 264, 5000), (200, 2056, 328), (64, 256, 128), (65, 264, 192), (200, 1032, 520),
                                    (513, 2816, 256), (1500, 40, 64), (2048, 4104, 64)])
 def test_dense(dev, R, N, K):
     """Without segments: a shared expert, its residual the very output."""
@@ -137,7 +138,8 @@ def test_mxfp8(dev, K, act):
     import moe_glue_amd as mg
 
     g = gen(dev, K)
-    for ns, N, pad in (([0, 1, 64, 65, 200], 48, 1), ([257, 0, 3], 272, 128), ([300], 1040, 1)):
+    for ns, N, pad in (([0, 1, 64, 65, 200], 48, 1), ([257, 0, 3], 272, 128), ([300], 1040, 1), ([17, 33, 65, 2], 4112, 1),
+                       ([130, 193, 257, 64], 18448, 16)):
         off, cnt, R = layout(ns, pad, dev, tail=2)
         x, xs = mx_tensor(g, R, K)
         w, ws = mx_tensor(g, len(ns), N, K)
@@ -207,7 +209,7 @@ def test_gradients(dev, case):
 
     g = gen(dev, 30 + case)
     ns = RAGGED[case]
-    for i, (N, K) in enumerate(WIDTHS):
+    for i, (N, K) in enumerate(WIDTHS + [(72, 4104), (64, 11016), (136, 11024)]):
         pad = (1, 128, 16)[i % 3]
         off, cnt, R = layout(ns, pad, dev, tail=4)
         E = len(ns)
@@ -266,7 +268,7 @@ def test_dense_gradients(dev):
     import moe_glue_amd as mg
 
     g = gen(dev, 9)
-    for R, N, K in ((1, 8, 8), (300, 264, 520), (5000, 16, 24)):
+    for R, N, K in ((1, 8, 8), (16, 1096, 512), (17, 200, 1544), (300, 264, 520), (5000, 16, 24)):
         x, dy, w = normal(g, R, K), normal(g, R, N), normal(g, N, K)
         want, slack = G.product(dy.double(), w.double().T)
         G.assert_within(mg.grouped_linear_grad_x(dy, w), want, G.rounded(want, slack), f"dx {R}")
