@@ -12,7 +12,8 @@ constexpr int kKMax = 16;
 // act = g s u with s = 1 / (1 + e^-g):
 //   du = dact g s,   dg = dact u s (1 + g (1 - s))
 // with 1 - s = e^-g s formed as s(-g), so that it keeps its digits for large g.
-// One 16-byte vector of each of gate, up and dact a lane, as moe_swiglu.
+// One 16-byte vector of each of gate, up and dact a lane, as moe_swiglu.  32768 x 768
+// with act: 48.6 us, 6.2 TB/s of HBM's 6.7.
 constexpr int kSwigluThreads = 64;
 
 template <bool ACT>
@@ -49,7 +50,9 @@ __global__ __launch_bounds__(kSwigluThreads) void swiglu_backward_kernel(const u
 // out[t] = sum_j w[t, j] y[dest]: dy[dest] = bf16(w dout[t]), dw[t, j] = <dout[t],
 // y[dest]>.  A workgroup takes one token: each lane holds its 16-byte vectors of
 // dout, reads the k rows' and writes the k gradients'; the k sums meet through
-// lane-group reductions and LDS.
+// lane-group reductions and LDS.  8192 x 7168, k = 8: 400 us, 4.9 TB/s, of as many bytes
+// written as read, in rows all over y; 64 to 896 lanes a token, other store hints and rows
+// asked for ahead all took 400 to 417.  (Narrow rows take one wave, so that none idles.)
 template <int THREADS, int KC>
 __global__ __launch_bounds__(THREADS) void combine_backward_kernel(const u32x4* __restrict__ dout,
                                                                    const u32x4* y, const float* __restrict__ w,
@@ -104,7 +107,7 @@ __global__ __launch_bounds__(THREADS) void combine_backward_kernel(const u32x4* 
 // ------------------------------------------------------------------ expand
 // x_expanded[dest] = x[t]: dx[t] = bf16(residual[t] + sum_j dx_expanded[dest]),
 // fp32 in j order.  One 16-byte vector of one token's row a lane, its k loads in
-// flight at once, as combine.
+// flight at once, as combine.  8192 x 7168, k = 8 with residual: 195 us, 6.0 TB/s.
 constexpr int kExpandThreads = 64;
 
 template <int KC>
@@ -139,7 +142,8 @@ __global__ __launch_bounds__(kExpandThreads) void expand_backward_kernel(const u
 // w = softmax over the k selected keys: ds_j = w_j (dw_j - sum_i w_i dw_i), the
 // gradient of the logit of expert topk_ids[t, j]; every other logit's is 0.  A
 // wave takes a row of dlogits: lane j < k holds slot j, and each lane writes the
-// experts e = lane + 64 i, looking for its own among the slots.
+// experts e = lane + 64 i, adding up its own among the slots.  8192 x 256: 6.9 us, most of it
+// latency.
 constexpr int kRouteThreads = 256;
 
 __global__ __launch_bounds__(kRouteThreads) void route_backward_kernel(const int32_t* __restrict__ topk_ids,
@@ -163,7 +167,7 @@ __global__ __launch_bounds__(kRouteThreads) void route_backward_kernel(const int
         for (int j = 0; j < k; ++j) {
             const int ij = __builtin_amdgcn_readlane(id, j);
             const float sj = __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, ds), j));
-            if (ij == e0 + lane) v = sj;
+            if (ij == e0 + lane) v += sj;
         }
         if (e0 + lane < E) dlogits[t * E + e0 + lane] = v;
     }

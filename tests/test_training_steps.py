@@ -71,6 +71,17 @@ def routed(g, T, E, k, pad):
     return logits, (mg.route_padded(logits, k, pad) if pad > 1 else mg.route(logits, k))
 
 
+def test_route_backward_same_expert_twice(dev):
+    """Not what route() gives; both slots' gradients are the expert's."""
+    import moe_glue_amd as mg
+
+    ids = torch.tensor([[2, 2, 0]], dtype=I32, device=dev)
+    w = torch.tensor([[0.5, 0.25, 0.25]], device=dev)
+    dw = torch.tensor([[4.0, 8.0, 0.0]], device=dev)
+    dl, _ = mg.route_backward(ids, w, dw, 70)     # mean 4: 0, 1, -1
+    assert dl[0, 2] == 1.0 and dl[0, 0] == -1.0 and dl.abs().sum() == 2.0
+
+
 @pytest.mark.parametrize("T,H,E,k,pad", [(1, 8, 1, 1, 1), (5, 64, 4, 2, 1), (33, 520, 8, 8, 16), (100, 2048, 64, 6, 128),
                                          (64, 4104, 20, 16, 1), (257, 512, 40, 9, 1), (700, 1032, 512, 3, 16)])
 def test_combine_and_expand_backward(dev, T, H, E, k, pad):
