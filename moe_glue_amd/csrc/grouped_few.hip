@@ -254,14 +254,14 @@ __device__ __forceinline__ void few_product(const GroupedArgs& g, const Tile& t,
         sum8(c + OUT_COLS, u);
         if (g.bias != nullptr) add8(u, load8(g.bias + (int64_t)t.e * g.N + out_cols + col));
         if (g.pre != nullptr) {
-            store8(g.pre + row * g.N + col, v);
-            store8(g.pre + row * g.N + out_cols + col, u);
+            store(g.pre + row * g.N + col, pack8(v));
+            store(g.pre + row * g.N + out_cols + col, pack8(u));
         }
 #pragma unroll
         for (int q = 0; q < 8; ++q) v[q] = silu_mul(v[q], u[q]);
     }
     if (g.residual != nullptr) add8(v, load8(g.residual + row * out_cols + col));
-    store8(g.out + row * out_cols + col, v);
+    store(g.out + row * out_cols + col, pack8(v));
 }
 
 template <int NC, bool BT, bool MX, bool SWIGLU>

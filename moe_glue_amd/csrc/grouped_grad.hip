@@ -9,7 +9,7 @@
 // other's products, and nothing waits for a store.  (Workgroups that stay and take tile
 // after tile, their loads running on into the next: 397 us for 128 experts' 1536 x 2048 of
 // 256 rows, since loads behind a tile's stores cannot be waited for without them; here
-// 367.)  db is summed from the fragments of dy, in the first column tiles.  Every
+// 355.)  db is summed from the fragments of dy, in the first column tiles.  Every
 // expert's gradient is written, zeros for one without rows; a tile is one workgroup's, so
 // the sums run in one order.
 #include "grouped.h"
@@ -177,20 +177,24 @@ __global__ __launch_bounds__(kThreads, 2) void grad_w_kernel(GroupedGradArgs g, 
             const float s = __builtin_bit_cast(float, across_rows(__builtin_bit_cast(uint32_t, sums[i])));
             if (lane < 16 && n < g.N) sums_out[n] = s;
         }
+        const int row = n0 + (wm * MT + i) * 16 + line_row();
 #pragma unroll
         for (int j = 0; j < NT; j += 2) {
-            const int k = k0 + (wn * NT + j) * 16 + pair_column();
+            const int k = k0 + (wn * NT + j) * 16 + line_column();
             float v[8];
             pair_values(acc[i][j], acc[i][j + 1], v);
-            if (n < g.N && k < g.K) {
-                const int64_t o = first + (int64_t)n * g.K + k;
-                if (WIDE || partial) {
-                    f32x4* d = reinterpret_cast<f32x4*>((partial ? g.partial : static_cast<float*>(g.dw)) + o);
+            const bool inside = row < g.N && k < g.K;
+            const int64_t o = first + (int64_t)row * g.K + k;
+            if (WIDE || partial) {
+                to_lines(v);
+                f32x4* d = reinterpret_cast<f32x4*>((partial ? g.partial : static_cast<float*>(g.dw)) + o);
+                if (inside) {
                     d[0] = f32x4{v[0], v[1], v[2], v[3]};
                     d[1] = f32x4{v[4], v[5], v[6], v[7]};
-                } else {
-                    *reinterpret_cast<u32x4*>(static_cast<uint16_t*>(g.dw) + o) = pack8(v);
                 }
+            } else {
+                const u32x4 b = to_lines(pack8(v));
+                if (inside) store(static_cast<uint16_t*>(g.dw) + o, b);
             }
         }
     }

@@ -224,18 +224,19 @@ __device__ __forceinline__ void product(const GroupedArgs& g, const Tile& t, uin
     // epilogue: eight columns of one row a lane, of two tiles of 16, once behind SwiGLU
     // and twice without.  Bias and residual are all asked for before the first use: one
     // after the other, behind the stores, they took a third of the time (8192 x 7168 x
-    // 2048 with a residual: 276 us, now 261).
+    // 2048 with a residual: 276 us, now 261).  Rows are loaded and stored line by line
+    // (to_lines()).
     constexpr int OUT = SWIGLU ? 1 : 2;
-    const int col = col0 + wn * 32 + pair_column();
+    const int bias_col = col0 + wn * 32 + pair_column(), col = col0 + wn * 32 + line_column();
     u32x4 bias[2], residual[2][MH][OUT];  // bias behind SwiGLU: of gate and up
     if (g.bias != nullptr) {
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
-            const int c = SWIGLU ? col : col + j * 128;
+            const int c = SWIGLU ? bias_col : bias_col + j * 128;
             if (c < out_cols) bias[j] = load8(g.bias + (int64_t)t.e * g.N + c + (SWIGLU ? j * out_cols : 0));
         }
     }
-    const auto row_of = [&](int h, int i) { return ((h * 2 + wm) * MH + i) * 16 + lane % 16; };
+    const auto row_of = [&](int h, int i) { return ((h * 2 + wm) * MH + i) * 16 + line_row(); };
     if (g.residual != nullptr) {
 #pragma unroll
         for (int h = 0; h < 2; ++h)
@@ -261,9 +262,12 @@ __device__ __forceinline__ void product(const GroupedArgs& g, const Tile& t, uin
                 if (g.bias != nullptr) add8(v[j], bias[j]);
             }
             if constexpr (SWIGLU) {
-                if (g.pre != nullptr && m < t.rows && col < out_cols) {
-                    store8(g.pre + row * g.N + col, v[0]);
-                    store8(g.pre + row * g.N + out_cols + col, v[1]);
+                if (g.pre != nullptr) {
+                    const u32x4 gate = to_lines(pack8(v[0])), up = to_lines(pack8(v[1]));
+                    if (m < t.rows && col < out_cols) {
+                        store(g.pre + row * g.N + col, gate);
+                        store(g.pre + row * g.N + out_cols + col, up);
+                    }
                 }
 #pragma unroll
                 for (int q = 0; q < 8; ++q) v[0][q] = silu_mul(v[0][q], v[1][q]);
@@ -271,10 +275,9 @@ __device__ __forceinline__ void product(const GroupedArgs& g, const Tile& t, uin
 #pragma unroll
             for (int j = 0; j < OUT; ++j) {
                 const int c = col + j * 128;
-                if (m < t.rows && c < out_cols) {
-                    if (g.residual != nullptr) add8(v[j], residual[h][i][j]);
-                    store8(g.out + row * out_cols + c, v[j]);
-                }
+                if (g.residual != nullptr) add8(v[j], from_lines(residual[h][i][j]));
+                const u32x4 o = to_lines(pack8(v[j]));
+                if (m < t.rows && c < out_cols) store(g.out + row * out_cols + c, o);
             }
         }
 }
