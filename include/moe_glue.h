@@ -457,8 +457,8 @@ typedef enum moe_act {
  * with act(h) = h (MOE_ACT_NONE, out has N columns) or silu(g) u of h = (g | u)
  * (MOE_ACT_SWIGLU, out has N/2 columns; silu as in moe_swiglu, of the unrounded h).
  * Each result is rounded once, to nearest even.  A row's result depends on the row
- * and its expert, and on how many rows the expert has only in the order of its
- * fp32 sums.  The same call gives the same bits every time.
+ * and its expert, and on the call's sizes and the other rows of the expert only in
+ * the order of its fp32 sums.  The same call gives the same bits every time.
  * Rows of no segment are neither read nor written: with the padded layout of
  * moe_route_padded give its expert_counts, or the padding rows are computed like
  * any other.  Segments must not overlap; entries outside [0, R] are taken as the

@@ -715,12 +715,13 @@ def _grouped(fn, x, x_scales, w, w_scales, offsets, counts, bias, act, residual,
         _need_gpu("w", w)
     E = _group_args(w.shape, offsets, counts, dev)
     N = w.shape[-2]
-    _check_shape("w", w, code, (*w.shape[:-1], K), dev)
+    lead = (N,) if offsets is None else (E, N)
+    _check_shape("w", w, code, (*lead, K), dev)
     if mx:
         if K % 32 != 0:
             raise MoEGlueArgumentError(2, f"K={K} is not a multiple of the 32-column block")
         _check_shape("x_scales", x_scales, torch.uint8, (R, K // 32), dev)
-        _check_shape("w_scales", w_scales, torch.uint8, (*w.shape[:-1], K // 32), dev)
+        _check_shape("w_scales", w_scales, torch.uint8, (*lead, K // 32), dev)
     if act not in ACTS:
         raise MoEGlueArgumentError(4, f"act={act!r} must be one of {list(ACTS)}")
     swiglu = act == "swiglu"
@@ -728,7 +729,7 @@ def _grouped(fn, x, x_scales, w, w_scales, offsets, counts, bias, act, residual,
         raise MoEGlueArgumentError(2, f"w has an odd number of rows {N}; expected gate rows, then up rows")
     shape = (R, N // 2 if swiglu else N)
     if bias is not None:
-        _check_shape("bias", bias, bf16, tuple(w.shape[:-1]), dev)
+        _check_shape("bias", bias, bf16, lead, dev)
     if residual is not None:
         _check_shape("residual", residual, bf16, shape, dev)
     if pre is not None:
@@ -781,7 +782,7 @@ def grouped_linear_grad_x(dy, w, offsets=None, counts=None, out=None):
         _need_gpu("w", w)
     E = _group_args(w.shape, offsets, counts, dev)
     K = w.shape[-1]
-    _check_shape("w", w, torch.bfloat16, (*w.shape[:-2], N, K), dev)
+    _check_shape("w", w, torch.bfloat16, (N, K) if offsets is None else (E, N, K), dev)
     if out is None:
         out = torch.empty((R, K), dtype=torch.bfloat16, device=dev)
     else:

@@ -1,6 +1,6 @@
 // Products of rows in expert order with their experts' weights, and their
-// gradients: the tile that the kernels of grouped_linear.hip and
-// grouped_grad.hip share.
+// gradients: what the kernels of grouped_linear.hip, grouped_few.hip and
+// grouped_grad.hip share, and the tile of the first.
 //
 // A workgroup of eight waves, two by four, computes D = A B^T over a tile of 64 MH
 // rows (m) by 256 columns (n) in fp32, with v_mfma_f32_16x16x32_bf16 (or the
@@ -416,7 +416,8 @@ __device__ __forceinline__ u32x4 to_lines(const u32x4& v) {
 }
 __device__ __forceinline__ void to_lines(float (&v)[8]) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = __builtin_bit_cast(float, from_lane(__builtin_bit_cast(uint32_t, v[i]), line_source()));
+    for (int i = 0; i < 8; ++i)
+        v[i] = __builtin_bit_cast(float, from_lane(__builtin_bit_cast(uint32_t, v[i]), line_source()));
 }
 // And back.
 __device__ __forceinline__ u32x4 from_lines(const u32x4& v) {

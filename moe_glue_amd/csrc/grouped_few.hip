@@ -290,7 +290,8 @@ hipError_t few_launch(const GroupedArgs& g, hipStream_t stream) {
 
 template <bool BT, bool MX, bool SWIGLU>
 hipError_t few(const GroupedArgs& g, int64_t tiles, hipStream_t stream) {
-    // 32 columns if that is a tile for every CU
+    // 32 columns if that is a tile for every CU (512 x 1024 x 7168: 22.0 us, 34.2 in tiles of 16;
+    // 32 x 2048 x 7168 in tiles of 16, one for every other CU: 14.3)
     if (tiles * 8 >= kCus) return few_launch<2, BT, MX, SWIGLU>(g, stream);
     return few_launch<1, BT, MX, SWIGLU>(g, stream);
 }
@@ -299,7 +300,8 @@ hipError_t few(const GroupedArgs& g, int64_t tiles, hipStream_t stream) {
 
 hipError_t launch_grouped_few(const GroupedArgs& g, bool transposed, bool swiglu, int64_t tiles, hipStream_t stream) {
     if (transposed) return few<true, false, false>(g, tiles, stream);
-    if (g.xs != nullptr) return swiglu ? few<false, true, true>(g, tiles, stream) : few<false, true, false>(g, tiles, stream);
+    if (g.xs != nullptr)
+        return swiglu ? few<false, true, true>(g, tiles, stream) : few<false, true, false>(g, tiles, stream);
     return swiglu ? few<false, false, true>(g, tiles, stream) : few<false, false, false>(g, tiles, stream);
 }
 
