@@ -51,8 +51,9 @@ __global__ __launch_bounds__(kSwigluThreads) void swiglu_backward_kernel(const u
 // y[dest]>.  A workgroup takes one token: each lane holds its 16-byte vectors of
 // dout, reads the k rows' and writes the k gradients'; the k sums meet through
 // lane-group reductions and LDS.  8192 x 7168, k = 8: 400 us, 4.9 TB/s, of as many bytes
-// written as read, in rows all over y; 64 to 896 lanes a token, other store hints and rows
-// asked for ahead all took 400 to 417.  (Rows of up to 512 columns take
+// written as read, in rows all over y (a stream of that mix in order: 6.6; rows taken in the order
+// of y would need the inverse map, which the call has not); 64 to 896 lanes a token, other store
+// hints and rows asked for ahead all took 400 to 417.  (Rows of up to 512 columns take
 // one wave: 8192 x 128, k = 8 10.0 us, 14.9 with four; 8192 x 512 26.2 and 28.3.)
 template <int THREADS, int KC>
 __global__ __launch_bounds__(THREADS) void combine_backward_kernel(const u32x4* __restrict__ dout,
