@@ -274,6 +274,7 @@ __device__ __forceinline__ void meet() {
     __builtin_amdgcn_s_barrier();
     asm volatile("" ::: "memory");
 }
+// This wave's LDS reads, and what it wrote to LDS itself (MXFP8 scale bytes), are done.
 __device__ __forceinline__ void reads_done() { asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory"); }
 // At most N of this wave's loads in flight.
 template <int N>
@@ -313,6 +314,7 @@ __device__ __forceinline__ void run_steps(int steps, const ReadA& read_a, const 
         load(q3, s, s);
     }
     loads_done<LEFT0 + STEP>();
+    reads_done();  // scale bytes that this wave wrote and others read
     meet();
     if (late) meet();
     const auto quarter = [&](auto ha, auto hb) {
