@@ -63,6 +63,10 @@ __device__ __forceinline__ Segment segment(const GroupedRows& g, int e) {
 // in units of 64 rows, dealt out evenly.
 __host__ __device__ __forceinline__ int row_tiles(int n, int whole) { return (n + whole - 1) / whole; }
 
+// Pieces of an expert's n rows, of up to `piece`; none has one too.  (n may be any int32: a
+// weight gradient's rows have no other limit.)
+__host__ __device__ __forceinline__ int pieces_of(int n, int piece) { return n > 0 ? (n - 1) / piece + 1 : 1; }
+
 struct Tile {
     int e;      // expert
     int first;  // first row

@@ -30,9 +30,6 @@ constexpr int kStages = 3;
 constexpr int kLoads = AOperand::LOADS + BOperand::LOADS;
 static_assert(2 * kStages * kStage <= kLdsBytes, "two workgroups a CU");
 
-// Pieces of an expert's n rows, of up to `piece`; none has one too.
-__device__ __forceinline__ int pieces_of(int n, int piece) { return max((n + piece - 1) / piece, 1); }
-
 // A piece of an expert, of `of`; the slots of the partial sums are numbered over the
 // experts that have several pieces, and slot is the expert's first.
 struct Piece {
@@ -97,7 +94,7 @@ __global__ __launch_bounds__(kThreads, 2) void grad_w_kernel(GroupedGradArgs g, 
         seg.n = min(seg.n - p.at * g.piece, g.piece);
     }
     const uint32_t lda = (uint32_t)g.N * 2, ldb = (uint32_t)g.K * 2;
-    const int steps = (seg.n + kStep - 1) / kStep;
+    const int steps = (int)(((uint32_t)seg.n + kStep - 1) / kStep);
     AOperand a;
     a.set(reinterpret_cast<const uint8_t*>(g.dy) + (int64_t)seg.first * lda + n0 * 2, (int64_t)seg.n * lda - n0 * 2,
           lda);
