@@ -706,26 +706,27 @@ moe_status check_k(const char* fn, int32_t T, int32_t k) {
     return MOE_OK;
 }
 
-// Segments, widths and tiles of the grouped products.
-moe_status check_grouped(const char* fn, const moe::GroupedRows& g, int32_t N, int32_t K, int64_t tiles) {
+// Segments and tiles of the grouped products.
+moe_status check_grouped(const char* fn, const moe::GroupedRows& g, int64_t tiles) {
     if (g.E < 1 || g.R < 0) return fail(MOE_ERR_SHAPE, "%s: E=%d must be >= 1 and R=%d >= 0", fn, g.E, g.R);
     if (g.E > MOE_E_MAX) return fail(MOE_ERR_UNSUPPORTED, "%s: E=%d exceeds %d", fn, g.E, MOE_E_MAX);
     if (g.offsets == nullptr && (g.E != 1 || g.counts != nullptr))
         return fail(MOE_ERR_NULL, "%s: without expert_offsets there is one expert (E=%d) and no expert_counts", fn, g.E);
     if (!aligned4(g.offsets) || !aligned4(g.counts))
         return fail(MOE_ERR_ALIGN, "%s: offsets and counts must be 4-byte aligned", fn);
-    if (N > MOE_GROUPED_WIDTH_MAX || K > MOE_GROUPED_WIDTH_MAX)
-        return fail(MOE_ERR_UNSUPPORTED, "%s: N=%d or K=%d exceeds %d", fn, N, K, MOE_GROUPED_WIDTH_MAX);
     if (tiles > MOE_GROUPED_TILES_MAX)
         return fail(MOE_ERR_UNSUPPORTED, "%s: %lld tiles exceed %d", fn, (long long)tiles, MOE_GROUPED_TILES_MAX);
     return MOE_OK;
 }
 
+// Before anything is computed from a width.
 moe_status check_grouped_width(const char* fn, const char* name, int32_t width, int32_t unit) {
     if (width < 1) return fail(MOE_ERR_SHAPE, "%s: %s=%d must be >= 1", fn, name, width);
     if (width % unit != 0)
         return fail(unit == 32 ? MOE_ERR_SHAPE : MOE_ERR_ALIGN, "%s: %s=%d is not a multiple of %d", fn, name, width,
                     unit);
+    if (width > MOE_GROUPED_WIDTH_MAX)
+        return fail(MOE_ERR_UNSUPPORTED, "%s: %s=%d exceeds %d", fn, name, width, MOE_GROUPED_WIDTH_MAX);
     return MOE_OK;
 }
 
@@ -733,7 +734,7 @@ moe_status check_grad_w(const char* fn, const moe::GroupedRows& rows, int32_t N,
     moe_status s = check_grouped_width(fn, "K", K, 8);
     if (s == MOE_OK) s = check_grouped_width(fn, "N", N, 8);
     if (s != MOE_OK) return s;
-    return check_grouped(fn, rows, N, K, moe::grouped_grad_w_tiles(rows, N, K));
+    return check_grouped(fn, rows, moe::grouped_grad_w_tiles(rows, N, K));
 }
 
 moe_status grouped_impl(const char* fn, const moe::GroupedArgs& g, bool mx, int act, void* stream) {
@@ -741,7 +742,7 @@ moe_status grouped_impl(const char* fn, const moe::GroupedArgs& g, bool mx, int 
     const bool swiglu = act == MOE_ACT_SWIGLU;
     moe_status s = check_grouped_width(fn, "K", g.K, mx ? 32 : 8);
     if (s == MOE_OK) s = check_grouped_width(fn, "N", g.N, swiglu ? 16 : 8);
-    if (s == MOE_OK) s = check_grouped(fn, g.rows, g.N, g.K, moe::grouped_linear_tiles(g.rows, g.N));
+    if (s == MOE_OK) s = check_grouped(fn, g.rows, moe::grouped_linear_tiles(g.rows, g.N));
     if (s != MOE_OK) return s;
     if (g.pre != nullptr && !swiglu) return fail(MOE_ERR_UNSUPPORTED, "%s: pre without an activation", fn);
     if (g.rows.R == 0) return ok();
@@ -785,7 +786,7 @@ moe_status moe_grouped_linear_grad_x(const uint16_t* dy, int32_t R, const int32_
     const moe::GroupedRows rows = {expert_offsets, expert_counts, E, R};
     moe_status s = check_grouped_width(fn, "K", K, 8);
     if (s == MOE_OK) s = check_grouped_width(fn, "N", N, 8);
-    if (s == MOE_OK) s = check_grouped(fn, rows, N, K, moe::grouped_linear_tiles(rows, K));
+    if (s == MOE_OK) s = check_grouped(fn, rows, moe::grouped_linear_tiles(rows, K));
     if (s != MOE_OK) return s;
     if (R == 0) return ok();
     if (!dy || !w || !dx) return fail(MOE_ERR_NULL, "%s: NULL tensor pointer", fn);
