@@ -148,7 +148,8 @@ __device__ __forceinline__ BufferWords buffer_words(const void* p, int64_t bytes
 // LDS read for one of what is in flight, whatever buffer it goes to, and waits for all
 // loads before it (dx of 32768 rows, 128 experts, 1536 x 2048: 336 us, 298 without).  There is
 // no register to write; waiting is the caller's (loads_done).  M0 holds the LDS address,
-// and the wait state is the one it asks for before a load to LDS.  A scalar register that a
+// and the wait state is the one it asks for before a load to LDS.  (M0 is reserved: the compiler
+// keeps nothing in it, and takes no clobber of it.)  A scalar register that a
 // vector instruction wrote may be read by a load five wait states later at the earliest, which
 // the compiler does not see to here: the buffers come from scalar arithmetic on values read
 // from lanes long before, and tests/test_grouped_listing.py follows every path to every load.
@@ -157,13 +158,13 @@ __device__ __forceinline__ void load_to_lds(const BufferWords& r, uint32_t lane,
     asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds" ::"s"(
                      (uint32_t)(uintptr_t)(MOE_LDS uint8_t*)lds),
                  "v"(lane), "s"(r), "s"(scalar)
-                 : "memory", "m0");
+                 : "memory");
 }
 __device__ __forceinline__ void load_dword_to_lds(const BufferWords& r, uint32_t lane, uint8_t* lds) {
     asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dword %1, %2, 0 offen lds" ::"s"(
                      (uint32_t)(uintptr_t)(MOE_LDS uint8_t*)lds),
                  "v"(lane), "s"(r)
-                 : "memory", "m0");
+                 : "memory");
 }
 
 // An operand with the summed index along its rows, of `ld` bytes each; load j of a
