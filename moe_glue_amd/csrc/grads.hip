@@ -200,6 +200,7 @@ __global__ __launch_bounds__(kBiasThreads) void route_bias_kernel(const float* _
     if (r == 0 && e < E) dbias[e] = s_sum[0][threadIdx.x];
 }
 
+// A launch holds fewer than 2^32 lanes: kSliceTokens tokens of up to 256.
 constexpr int64_t kSliceTokens = 1 << 22;
 
 template <int THREADS>
@@ -208,7 +209,6 @@ hipError_t combine_threads(const void* dout, const void* y, const float* w, cons
     const auto* yv = static_cast<const u32x4*>(y);
     auto* o = static_cast<u32x4*>(dy);
     const uint32_t H8 = (uint32_t)H / 8;
-    // a launch holds fewer than 2^32 lanes: kSliceTokens tokens of up to 256
     for (int64_t t = 0; t < T; t += kSliceTokens) {
         const uint32_t n = (uint32_t)(T - t < kSliceTokens ? T - t : kSliceTokens);
         const auto* d = static_cast<const u32x4*>(dout) + t * H8;
@@ -267,10 +267,11 @@ hipError_t launch_expand_backward(const void* dx_expanded, const int32_t* dest_o
 
 hipError_t launch_route_backward(const int32_t* topk_ids, const float* topk_weights, const float* dweights, int T,
                                  int E, int k, float* dlogits, float* dbias, hipStream_t stream) {
-    if (T > 0) {
-        const uint32_t rows = kRouteThreads / kWave;
-        route_backward_kernel<<<((uint32_t)T + rows - 1) / rows, kRouteThreads, 0, stream>>>(
-            topk_ids, topk_weights, dweights, T, E, k, dlogits);
+    const uint32_t rows = kRouteThreads / kWave;
+    for (int64_t t = 0; t < T; t += kSliceTokens) {
+        const int n = (int)(T - t < kSliceTokens ? T - t : kSliceTokens);
+        route_backward_kernel<<<((uint32_t)n + rows - 1) / rows, kRouteThreads, 0, stream>>>(
+            topk_ids + t * k, topk_weights + t * k, dweights + t * k, n, E, k, dlogits + t * E);
         const hipError_t e = hipGetLastError();
         if (e != hipSuccess) return e;
     }

@@ -25,6 +25,37 @@ def test_sizes_host(tmp_path):
     assert out.returncode == 0 and out.stdout.endswith("ok\n"), f"status {out.returncode} behind: {out.stdout}{out.stderr}"
 
 
+def test_launches_host(tmp_path):
+    """Every launch of the largest calls fits the runtime's limit on lanes, and a routing
+    gradient's cover its tokens (tests/host/gradient_launches_check.cpp)."""
+    exe = tmp_path / "gradient_launches_check"
+    csrc = os.path.join(ROOT, "moe_glue_amd", "csrc")
+    subprocess.run(["hipcc", "-O1", "-std=c++17", "-x", "hip", "--offload-arch=gfx950", "--cuda-host-only",
+                    "-I", os.path.join(ROOT, "include"), "-I", csrc,
+                    os.path.join(ROOT, "tests", "host", "gradient_launches_check.cpp"),
+                    *(os.path.join(csrc, f) for f in ("api.cpp", "grouped_linear.hip", "grouped_few.hip",
+                                                      "grouped_grad.hip", "grads.hip")),
+                    "-Wl,--unresolved-symbols=ignore-all", "-o", str(exe)], check=True, capture_output=True)
+    out = subprocess.run([str(exe)], capture_output=True, text=True, timeout=300)
+    assert out.returncode == 0 and out.stdout.endswith("ok\n"), f"status {out.returncode}: {out.stdout}{out.stderr}"
+
+
+@pytest.mark.gpu
+def test_routing_gradient_of_more_tokens_than_a_launch_holds():
+    """2^26 + 3 tokens of 64 lanes each are more than 2^32.  With k = 2, weights 1/2 and dw =
+    (a, b) the gradients are +- (a - b) / 4, and all are whole numbers of 32nds here."""
+    import moe_glue_amd as mg
+
+    dev, T = "cuda:0", 2 ** 26 + 3
+    at = torch.arange(T, device=dev, dtype=torch.int32)
+    ids = torch.stack((at % 2, 1 - at % 2), 1)
+    dw = torch.stack((at % 61, at % 7), 1).float() / 8
+    dlogits, none = mg.route_backward(ids, torch.full((T, 2), 0.5, device=dev), dw, 2)
+    want = (dw[:, 0] - dw[:, 1]) / 4
+    assert none is None and torch.equal(dlogits.gather(1, ids[:, :1].long())[:, 0], want)
+    assert torch.equal(dlogits.gather(1, ids[:, 1:].long())[:, 0], -want)
+
+
 @pytest.mark.gpu
 def test_weight_gradient_of_the_most_rows():
     """2^31 - 8 rows of ones, the last 64: each piece's sums and the joined ones are whole
