@@ -28,7 +28,9 @@ Four calls, each a thin wrapper over the C ABI of the HIP library
                                        gradients of the other steps
 
 Tensors are torch CUDA (HIP) tensors; bf16 tensors use torch.bfloat16.  Work
-is enqueued on torch's current stream and nothing synchronises.  Every call
+is enqueued on torch's current stream and nothing synchronises.  No call records an
+autograd graph, whether its inputs require gradients or not: a backward pass makes the
+gradients' calls itself.  Every call
 accepts preallocated outputs (``out=`` / the route output dict) so a caller
 can run the path without allocating.
 """

@@ -45,7 +45,9 @@ typedef int i32x8 __attribute__((ext_vector_type(8)));
 constexpr int kGroupedThreads = 512;
 constexpr int kLdsBytes = 160 * 1024;
 constexpr int kStepBytes = 128;             // of a row, per step
-constexpr uint32_t kPastEnd = 0x80000000u;  // an offset past the end of every buffer
+// An offset past the end of every buffer.  (The range check takes lane's and scalar's offsets
+// together and does not wrap: a scalar offset beyond a short buffer reads zeros too.  Measured.)
+constexpr uint32_t kPastEnd = 0x80000000u;
 
 // ---------------------------------------------------------------- segments
 // Rows of expert e: [first, first + n), inside [0, R) whatever the arrays hold.
@@ -408,7 +410,8 @@ __device__ __forceinline__ int pair_column() {
 // them: lane l has piece l % 4 of row l / 4 (line_row(), line_column()), so that the four
 // lanes of a quad stay inside a line.  Left where they are, with neighbouring lanes in different
 // rows, each store or load of a wave holds the CU's address path for 64 clocks, not 16
-// (weight gradients of 128 experts, 1536 x 2048: 367 us, 355 so; fp32, skewed: 376 and 362).
+// (weight gradients of 128 experts, 1536 x 2048: 367 us, 355 so in the same run; fp32, skewed: 376
+// and 362.  fp32's two stores of a lane leave every other 16 bytes of a line to each other.)
 __device__ __forceinline__ int line_row() { return (int)(threadIdx.x % kWave) / 4; }
 __device__ __forceinline__ int line_column() { return (int)(threadIdx.x % 4) * 8; }
 __device__ __forceinline__ uint32_t from_lane(uint32_t v, int lane) {

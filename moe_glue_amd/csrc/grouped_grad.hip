@@ -9,7 +9,8 @@
 // other's products, and nothing waits for a store.  (Workgroups that stay and take tile
 // after tile, their loads running on into the next: 397 us for 128 experts' 1536 x 2048 of
 // 256 rows, since loads behind a tile's stores cannot be waited for without them; here
-// 355.)  db is summed from the fragments of dy, in the first column tiles.  Every
+// 355 in the same run, and 359 in a trace of 60 passes.)  Within a wave nothing overlaps: matrix
+// cores are busy 28 % of a busy CU's cycles, LDS 21 %.  db is summed from the fragments of dy, in the first column tiles.  Every
 // expert's gradient is written, zeros for one without rows; a tile is one workgroup's, so
 // the sums run in one order.
 #include "grouped.h"
@@ -271,9 +272,17 @@ hipError_t launch(const GroupedGradArgs& g, hipStream_t stream) {
 // Rows of a piece: those whose steps are as many as one of the workgroups that run at a
 // time would have if all tiles' steps were spread evenly, 1024 at least: below that
 // joining costs more than it gives.  0: whole experts, where none can have more rows, or
-// an expert's tiles are many enough to be busy alone.  (34 skewed experts of 31239 rows,
-// 784 x 328 in fp32: 369 us whole, 79 in pieces; one of 3059 rows, 224 x 4232, with dx: 79
-// and 47.  But 128 even experts of 32768 rows, 1536 x 2048, 96 tiles each: 367 and 386.)
+// an expert has kTilesMax tiles or more.  Below that pieces win (whole and in pieces, us: 34
+// skewed experts of 31239 rows, 784 x 328 in fp32 369 and 79; one of 3059 rows, 224 x 4232, with
+// dx, 79 and 47).  From there on it goes by what the rule does not look at, the number of experts
+// and how uneven they are:
+//   128 even experts, 32768 rows, 1536 x 2048 (96 tiles): 348 and 366, since nothing is cut and the
+//     search and the join are paid; one expert, 8192 rows, 2048 x 7168 (448 tiles): 238 and 248;
+//   one expert, 32768 rows: 1024 x 2048 (64 tiles) 624 and 167, 1536 x 2048 629 and 240; 8192 rows,
+//     4096 x 1408 in fp32 (192 tiles) 163 and 135; 4096 rows, 2048 x 2048 (128 tiles) 82 and 62;
+//   8 experts, 32768 rows, 1536 x 2048: even 209 and 206, skewed 392 and 265; 128 skewed ones 602
+//     and 449; 64 skewed ones, 6138 rows, 4096 x 1408 in fp32 366 and 357.
+// So few or uneven experts of many rows lose by the whole ones, up to fourfold.
 constexpr int kSlots = 512, kPieceMin = 1024, kTilesMax = 64;
 int piece_rows(const GroupedRows& g, int N, int K) {
     const int64_t per_expert = (int64_t)((N + kTileN - 1) / kTileN) * ((K + kTileK - 1) / kTileK);

@@ -2,12 +2,26 @@
 // gfx950: rows in expert order times their experts' weights, with bias, SwiGLU
 // and residual in the epilogue (forward), or times the weights' rows (dx = dy W).
 //
+// What bounds the products of many rows: neither the matrix cores nor LDS is near full (busy 31
+// to 57 % and 15 to 30 % of a busy CU's cycles, bank conflicts 4 % at most); waves stand at
+// waits and barriers for 26 to 44 % of theirs, and one workgroup a CU leaves a tile's
+// first loads and its epilogue uncovered.  32768 x 1536 x 2048 over 128 experts 253 to 293 us by how
+// long the card has been under load, 8192 x 7168 x 2048 222 to 241.
+//
 // MXFP8 operands are multiplied by the block-scaled instruction, at twice bf16's rate.  Its
-// accumulators are fp32, but it adds eight neighbours along k in fixed point, cutting off what
-// lies 2^-13 below the power of two of the largest (measured: of 2^16 - 2^16 + 2^j in one eight
-// 2^3 is kept and 2^2 is not).  The alternative, products of bf16 values, rounds nothing there and
-// takes twice the matrix time and bytes; a term at the cut is 2^-13 of one product of a sum
-// that is rounded to 2^-9 of itself.
+// accumulators are fp32, but it adds eight neighbours along k in fixed point: of each product
+// it cuts off, towards zero, what lies 2^-13 below the power of two of the largest.  (Measured:
+// of 2^16 - 2^16 + 2^j in one eight 2^3 is kept and 2^2 is not, and sums formed in 64 bits with
+// this cut give the kernel's every output of 256 x 256 x 2048 and 192 x 256 x 4096 normal ones.)
+// Those sums are off by 1.5e-5 of their rms, 2.3e-6 of sum |x w| at the worst; the outputs' own
+// rounding is 1.7e-3, and with fp32 sums it is the same to four digits.  Where the sum cancels the cut
+// shows.  The way that keeps every product is moe_grouped_linear on the values, which are exact in
+// bf16 as far as its exponents reach: 32768 x 1536 x 2048 over 128 experts 253 us, 161 in MXFP8.
+//
+// Scale rows that are not whole aligned dwords (K % 128 != 0, or a pointer off one) pass through
+// registers, four byte loads a lane, whose wait every fourth step empties the loads in flight:
+// 32768 x 1536 over 128 experts, K = 2880: 294 us, where 2816 takes 207 and 2944 219; dense 8192 x
+// 7168: 212, 167 and 174.
 #include "grouped.h"
 
 namespace moe {
