@@ -10,9 +10,9 @@
 // after tile, their loads running on into the next: 397 us for 128 experts' 1536 x 2048 of
 // 256 rows, since loads behind a tile's stores cannot be waited for without them; here
 // 355 in the same run, and 359 in a trace of 60 passes.)  Within a wave nothing overlaps: matrix
-// cores are busy 28 % of a busy CU's cycles, LDS 21 %.  db is summed from the fragments of dy, in the first column tiles.  Every
-// expert's gradient is written, zeros for one without rows; a tile is one workgroup's, so
-// the sums run in one order.
+// cores are busy 28 % of a busy CU's cycles, LDS 21 %.  db is summed from the fragments of dy,
+// in the first column tiles.  Every expert's gradient is written, zeros for one without rows;
+// a tile is one workgroup's, so the sums run in one order.
 #include "grouped.h"
 
 namespace moe {
