@@ -488,8 +488,8 @@ moe_status moe_grouped_linear(const uint16_t* x, int32_t R, const int32_t* exper
  * power of two of the eight's largest: of each of the others less than 2^-13 of that
  * largest, towards zero; the rest of the sum is fp32.  (Of normal values, K = 2048, the
  * sums are off by 1.5e-5 of their rms, a hundredth of the result's rounding.)  Where sums
- * cancel and every product counts, moe_grouped_linear on the values keeps them: each is
- * a bf16 value as long as its exponent is one of bf16's.
+ * cancel and every product counts, moe_grouped_linear on the values keeps them to fp32's 24
+ * bits: each is a bf16 value as long as its exponent is one of bf16's.
  * x uint8 [R, K], x_scales uint8 [R, K/32], w uint8 [E, N, K], w_scales uint8
  * [E, N, K/32]; K % 32 == 0; codes 16-byte aligned, scales at any byte.  Otherwise
  * as moe_grouped_linear. */
